@@ -119,6 +119,22 @@ typedef struct {
  * on TT_OK; release it with tt_block_attn_plan_destroy. */
 TT_API tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_plan_t* out_plan);
 
+/* A plan for a layer with a sliding window over its context and a few first tokens that stay
+ * visible (sinks).  Every attention call of such a plan -- decode, paged, host, tree, quantised
+ * cache, block-causal and its backward -- sees, of the L committed positions in front of the
+ * block, only
+ *     { c : 0 <= c < L, c < sinks or c >= L - window }
+ * next to the block's own keys (L = ctx_lens[n] for decode, S*b for block b of a block-causal
+ * call).  The window slides with the block: all S rows of a block see the same context, and with
+ * S = 1 it is the usual per-token window.  Positions outside are not read, except that a paged
+ * call may load (and ignore) up to 63 rows in front of the window, within the window's first page.
+ * A call's cost goes with window + sinks, not with L.
+ *   window  >= 0; 0: no window (the plan of tt_block_attn_plan; sinks must be 0)
+ *   sinks   >= 0; positions that lie in both sets count once
+ * Otherwise as tt_block_attn_plan; TT_TCGEN05_VARIANT is ignored (the default form runs). */
+TT_API tt_status_t tt_block_attn_plan_window(const tt_block_attn_desc* desc, int window, int sinks, int device,
+                                             tt_plan_t* out_plan);
+
 TT_API void tt_block_attn_plan_destroy(tt_plan_t plan);
 
 TT_API tt_status_t tt_block_attn_plan_get_info(tt_plan_t plan, tt_plan_info* info);
@@ -179,6 +195,82 @@ TT_API tt_status_t tt_block_attn_paged(tt_plan_t plan, const void* q, const void
                                 int32_t page_size, int32_t pages_per_seq, const void* k_blk,
                                 const void* v_blk, const int32_t* ctx_lens, float* out, float* lse,
                                 tt_stream_t stream);
+
+/* Decode in which the block's S rows are a TREE of drafted tokens (a draft that is verified in one
+ * call): row t sees the whole visible context, itself and its ancestors, and nothing else of the
+ * block.  The framework's own verifier is the context tower, which keeps its LM head (kept for
+ * scoring and speculative decoding: paperfeed review of arXiv 2606.26493, "What this changes, and
+ * what to be skeptical of").
+ *   parents [B, S] int32 (device): parents[n][t] is the row that row t hangs on, 0 <= parent < t;
+ *           -1: it hangs on the last committed token; -2: row t is absent (a sequence that
+ *           drafted fewer than S tokens).  A row whose ancestor is absent is absent too.
+ * An absent row's output is 0 and its lse -inf, and its q, k_blk and v_blk may hold anything.  An
+ * entry >= t or < -2 is flagged TT_ERR_DEVICE_ARG and its row taken as absent.
+ * Everything else as tt_block_attn; runs the default tcgen05 kernel (64-key tiles) or the
+ * mma.sync kernel, as the plan chose. */
+TT_API tt_status_t tt_block_attn_tree(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx,
+                                      const void* k_blk, const void* v_blk, const int32_t* ctx_lens,
+                                      const int32_t* parents, float* out, float* lse, tt_stream_t stream);
+/* The same over a paged context cache (pages as tt_block_attn_paged). */
+TT_API tt_status_t tt_block_attn_tree_paged(tt_plan_t plan, const void* q, const void* k_pages,
+                                            const void* v_pages, const int32_t* page_table, int32_t num_pages,
+                                            int32_t page_size, int32_t pages_per_seq, const void* k_blk,
+                                            const void* v_blk, const int32_t* ctx_lens, const int32_t* parents,
+                                            float* out, float* lse, tt_stream_t stream);
+
+/* A context cache in microscaled 8-bit floating point: e4m3 values with one scale per 32 elements
+ * of the head dimension, a power of two 2^e held as the byte e + 127 (0..254).  An element's value
+ * is e4m3 * 2^e, which bf16 represents exactly (down to bf16's subnormals), so attention over the
+ * cache is attention over these values without a further rounding.  1 + 1/32 bytes per element.
+ * page_table NULL: contiguous slabs over the plan's ctx_capacity
+ *   k, v              [B, Hkv, Lcap, D]      e4m3
+ *   k_scale, v_scale  [B, Hkv, Lcap, D / 32] uint8
+ * otherwise pages, addressed as in tt_block_attn_paged (page_size a power of two in [16, 65536])
+ *   k, v              [num_pages, Hkv, page_size, D]
+ *   k_scale, v_scale  [num_pages, Hkv, page_size, D / 32]
+ *   page_table        [B, pages_per_seq] int32 (device)
+ * All four buffers 16-byte aligned, the table 4-byte. */
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const int32_t* page_table;
+  int32_t num_pages;
+  int32_t page_size;
+  int32_t pages_per_seq;
+} tt_mx_cache;
+
+/* Quantise new rows as they are written into the cache: position L_n + t of sequence n takes row t
+ * of k_new / v_new, t < counts[n], and then, when `advance` is non-zero, ctx_lens[n] += counts[n].
+ *   k_new, v_new [B, rows, Hkv, D] bf16;  counts [B] int32 (device) or NULL: `rows` for every
+ *   sequence;  ctx_lens [B] int32 (device), read (and advanced) in place
+ * Per 32 elements: amax = the largest finite magnitude, e = the least integer >= -127 with
+ * amax <= 448 * 2^e, value = e4m3(x * 2^-e) rounded to nearest even.  An infinity saturates to
+ * +-448 * 2^e, a NaN is stored as e4m3's NaN.  Rows outside [L_n, L_n + counts[n]) are not touched.
+ * `rows` need not be the plan's block size: a committed block, an accepted draft or a whole prompt.
+ * A sequence with counts[n] outside [0, rows], L_n < 0 or no room is left untouched (rows and
+ * length) and flagged TT_ERR_DEVICE_ARG; so is a row whose page lies outside the pool (that row
+ * only).  Uses the plan's B, Hkv, D (and ctx_capacity for slabs); B <= 65535. */
+TT_API tt_status_t tt_kv_append_mx(tt_plan_t plan, const void* k_new, const void* v_new, int rows,
+                                   const int32_t* counts, const tt_mx_cache* cache, int32_t* ctx_lens, int advance,
+                                   tt_stream_t stream);
+
+/* Read rows of the cache back as bf16: position starts[n] + t of sequence n, t < rows, goes to
+ * k_out / v_out [B, Hkv, rows, D] (the layout of a context slab) where it lies below ctx_lens[n];
+ * other rows of the outputs are left as they were.  The value is rounded to nearest even (exact
+ * above bf16's subnormals); e4m3's NaN reads as NaN.  starts [B] int32 (device) or NULL: 0.
+ * A negative start (nothing is read), a length outside [0, capacity] (clamped) and a page outside
+ * the pool (its rows are skipped) are flagged TT_ERR_DEVICE_ARG.  B <= 65535. */
+TT_API tt_status_t tt_kv_read_mx(tt_plan_t plan, const tt_mx_cache* cache, const int32_t* ctx_lens,
+                                 const int32_t* starts, int rows, void* k_out, void* v_out, tt_stream_t stream);
+
+/* Decode block attention over the quantised cache: tt_block_attn (or tt_block_attn_paged) with the
+ * context's keys and values taken from `cache`; q, k_blk and v_blk stay bf16.
+ *   parents  NULL: a bidirectional block; otherwise a drafted tree as in tt_block_attn_tree */
+TT_API tt_status_t tt_block_attn_mx(tt_plan_t plan, const void* q, const tt_mx_cache* cache, const void* k_blk,
+                                    const void* v_blk, const int32_t* ctx_lens, const int32_t* parents, float* out,
+                                    float* lse, tt_stream_t stream);
 
 /* Block-causal training / prefill form over whole sequences of length N = seq_len.
  *   q      [B, N, Hq, D]  bf16      out [B, N, Hq, D] fp32 (bf16 on a TT_PLAN_OUT_BF16 plan)

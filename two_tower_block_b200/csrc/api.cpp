@@ -8,6 +8,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -15,6 +16,7 @@
 #include "../../include/tt_block_attn.h"
 #include "problem.h"
 #include "kv_append.h"
+#include "kv_mx.h"
 #include "attn_bwd.h"
 #include "unmask.h"
 #include "errbits.h"
@@ -80,6 +82,7 @@ constexpr int kProfMax = 4096;
 
 struct tt_plan_s {
   tt_block_attn_desc desc;
+  int window = 0, sinks = 0;   // sliding window of the context (0: none) and first tokens kept
   int device = 0;
   int sm_count = 0;
   int kernel = TT_KERNEL_MMA_SYNC;
@@ -102,6 +105,7 @@ struct tt_plan_s {
   // so that every range of a launch has seen the same number of launches
   unsigned* arr_decode = nullptr;
   unsigned* arr_causal = nullptr;
+  unsigned* ticket = nullptr;   // block arrivals of a cache write that advances the lengths (always back at 0)
   bool fused_combine = false;   // block-causal calls combine in the attention kernel's tail
   bool fused_decode = false;    // decode and paged calls do
   int* causal_pref = nullptr;
@@ -132,6 +136,7 @@ struct DeviceGuard {
 };
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 void prof_mark(tt_plan_t plan, int kid, cudaStream_t s, bool begin) {
   if (!plan->prof_on) return;
@@ -172,13 +177,19 @@ tt::Problem base_problem(tt_plan_t plan) {
   p.variant = plan->variant;
   p.arrivals = nullptr;
   p.out_bf16 = (d.flags & TT_PLAN_OUT_BF16) ? 1 : 0;
+  p.window = plan->window;
+  p.sinks = plan->sinks;
+  p.win_align = 1;
+  p.parents = nullptr;
   return p;
 }
 
 tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s) {
   cudaError_t e;
   prof_mark(plan, 0, s, true);
-  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 3) {
+  if (p.k_scale) {
+    e = tt::launch_attn_mma_sync(p, s);
+  } else if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 3) {
     e = tt::launch_attn_2sm(p, s);
   } else if (plan->kernel == TT_KERNEL_TCGEN05) {
     tt::TmaMaps maps;
@@ -290,6 +301,134 @@ std::vector<long long> weighted_causal_starts(const std::vector<int>& pref, long
   return tab;
 }
 
+// The context of a decode call: contiguous slabs, or pages; bf16, or e4m3 with scales.
+struct CtxCache {
+  const void *k, *v;
+  const uint8_t *k_scale, *v_scale;   // null: bf16
+  bool paged;
+  const int32_t* table;
+  int num_pages, page_size, pages_per_seq;
+};
+
+tt_status_t page_args(int num_pages, int page_size, int pages_per_seq) {
+  if (page_size < 16 || page_size > (1 << 16) || (page_size & (page_size - 1)))
+    return fail(TT_ERR_INVALID_ARG, "page_size must be a power of two in [16, 65536]");
+  if (num_pages < 0 || pages_per_seq < 0) return fail(TT_ERR_INVALID_ARG, "negative num_pages or pages_per_seq");
+  return TT_OK;
+}
+tt_status_t page_range(const tt_block_attn_desc& d, int num_pages, int page_size, int pages_per_seq) {
+  if ((long long)pages_per_seq * page_size > (1ll << 31) - 1 ||
+      (long long)num_pages * d.num_kv_heads * page_size > (1ll << 31) - 1)
+    return fail(TT_ERR_UNSUPPORTED, "page pool or page table too large (rows beyond 2^31)");
+  return TT_OK;
+}
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+// Every decode form: checks the arguments and launches.  parents null: a bidirectional block.
+tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const void* k_blk, const void* v_blk,
+                        const int32_t* ctx_lens, const int32_t* parents, float* out, float* lse,
+                        tt_stream_t stream) {
+  if (c.paged) {
+    const tt_status_t st = page_args(c.num_pages, c.page_size, c.pages_per_seq);
+    if (st != TT_OK) return st;
+  }
+  if (!plan) return fail(TT_ERR_INVALID_ARG, "null plan");
+  const tt_block_attn_desc& d = plan->desc;
+  if (c.paged) {
+    const tt_status_t st = page_range(d, c.num_pages, c.page_size, c.pages_per_seq);
+    if (st != TT_OK) return st;
+  }
+  if (d.batch == 0) return TT_OK;
+  if (!q || !k_blk || !v_blk || !ctx_lens || !out) return fail(TT_ERR_INVALID_ARG, "null tensor pointer");
+  if (c.paged) {
+    if (c.pages_per_seq > 0 && (!c.table || !c.k || !c.v || c.num_pages < 1))
+      return fail(TT_ERR_INVALID_ARG, "pages_per_seq > 0 needs a page table and non-empty pools");
+  } else if (d.ctx_capacity > 0 && (!c.k || !c.v)) {
+    return fail(TT_ERR_INVALID_ARG, "null context pointer");
+  }
+  if (!aligned16(q) || !aligned16(c.k) || !aligned16(c.v) || !aligned16(c.k_scale) || !aligned16(c.v_scale) ||
+      !aligned16(k_blk) || !aligned16(v_blk) || !aligned16(out) || !aligned16(lse) || !aligned4(ctx_lens) ||
+      !aligned4(c.table) || !aligned4(parents))
+    return fail(TT_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
+  DeviceGuard guard(plan->device);
+  tt::Problem p = base_problem(plan);
+  p.C = plan->C_decode;
+  p.arrivals = plan->fused_decode ? plan->arr_decode : nullptr;
+  p.mode = tt::kDecode;
+  p.NB = 1;
+  const bool mx = c.k_scale != nullptr;
+  if (c.paged || parents || mx) {
+    // these forms live in the default tcgen05 kernel (and the mma.sync one)
+    p.variant = 0;
+    if (plan->variant == 3) p.C = plan->C_paged;
+  }
+  if (parents || mx || (c.paged && p.window > 0)) {
+    p.key_tile = tt::kTcgen05KeyTile;   // and in its 64-key form
+    p.blk_tiles = tt::ceil_div(d.block_size, p.key_tile);
+  }
+  if (c.paged) {
+    p.ctx_stride = c.pages_per_seq * c.page_size;
+    p.page_shift = log2_of(c.page_size);
+    p.pages_per_seq = c.pages_per_seq;
+    p.num_pages = c.num_pages;
+    p.page_table = c.pages_per_seq > 0 ? c.table : nullptr;
+    // the tcgen05 kernel loads whole slices of a page: its window run starts at one
+    if (plan->kernel == TT_KERNEL_TCGEN05 && !mx) p.win_align = std::min(c.page_size, p.key_tile);
+  } else {
+    p.ctx_stride = d.ctx_capacity;
+  }
+  if (mx) p.arrivals = nullptr;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_ctx = static_cast<const __nv_bfloat16*>(c.k);
+  p.v_ctx = static_cast<const __nv_bfloat16*>(c.v);
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
+  p.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
+  p.ctx_lens = ctx_lens;
+  p.parents = parents;
+  p.out = out;
+  p.lse = lse;
+  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+// The rows of a quantised cache as the write and read-back kernels take them, checked.
+tt_status_t mx_rows(tt_plan_t plan, const tt_mx_cache* cache, tt::MxRows* m) {
+  if (!cache) return fail(TT_ERR_INVALID_ARG, "null cache");
+  if (cache->page_table) {
+    const tt_status_t st = page_args(cache->num_pages, cache->page_size, cache->pages_per_seq);
+    if (st != TT_OK) return st;
+  }
+  if (!plan) return fail(TT_ERR_INVALID_ARG, "null plan");
+  const tt_block_attn_desc& d = plan->desc;
+  if (d.batch > 65535) return fail(TT_ERR_UNSUPPORTED, "cache writes and reads take at most 65535 sequences");
+  if (cache->page_table) {
+    const tt_status_t st = page_range(d, cache->num_pages, cache->page_size, cache->pages_per_seq);
+    if (st != TT_OK) return st;
+  }
+  if (d.batch > 0 && (!cache->k || !cache->v || !cache->k_scale || !cache->v_scale))
+    return fail(TT_ERR_INVALID_ARG, "null cache pointer");
+  if (!aligned16(cache->k) || !aligned16(cache->v) || !aligned16(cache->k_scale) || !aligned16(cache->v_scale) ||
+      !aligned4(cache->page_table))
+    return fail(TT_ERR_INVALID_ARG, "cache pointer not 16-byte aligned");
+  m->k = static_cast<uint8_t*>(cache->k);
+  m->v = static_cast<uint8_t*>(cache->v);
+  m->k_scale = cache->k_scale;
+  m->v_scale = cache->v_scale;
+  m->table = cache->page_table;
+  m->page_shift = cache->page_table ? log2_of(cache->page_size) : 0;
+  m->pages_per_seq = cache->pages_per_seq;
+  m->num_pages = cache->num_pages;
+  m->cap = cache->page_table ? cache->pages_per_seq * cache->page_size : d.ctx_capacity;
+  m->Hkv = d.num_kv_heads;
+  m->D = d.head_dim;
+  return TT_OK;
+}
+
 std::vector<long long> causal_range_table(const tt_plan_s* P, const std::vector<int>& pref,
                                           const tt_block_attn_desc& d) {
   if (pref.empty() || P->kernel != TT_KERNEL_TCGEN05 || P->variant != 0) return {};
@@ -298,25 +437,7 @@ std::vector<long long> causal_range_table(const tt_plan_s* P, const std::vector<
   return weighted_causal_starts(pref, (long long)d.batch * d.num_kv_heads, P->C, H);
 }
 
-}  // namespace
-
-extern "C" {
-
-const char* tt_status_string(tt_status_t s) {
-  switch (s) {
-    case TT_OK: return "ok";
-    case TT_ERR_INVALID_ARG: return "invalid argument";
-    case TT_ERR_UNSUPPORTED: return "unsupported configuration";
-    case TT_ERR_CUDA: return "CUDA error";
-    case TT_ERR_DEVICE_ARG: return "device-side argument error (ctx_lens out of range)";
-    case TT_ERR_TIMEOUT: return "device-side pipeline wait timed out";
-  }
-  return "unknown status";
-}
-
-const char* tt_last_error_detail(void) { return g_detail.c_str(); }
-
-tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_plan_t* out_plan) {
+tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int device, tt_plan_t* out_plan) {
   g_detail.clear();
   if (!desc || !out_plan) return fail(TT_ERR_INVALID_ARG, "null descriptor or output pointer");
   const tt_block_attn_desc d = *desc;
@@ -328,6 +449,8 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
   if (d.seq_len % d.block_size) return fail(TT_ERR_INVALID_ARG, "seq_len % block_size != 0");
   if (d.kernel < TT_KERNEL_AUTO || d.kernel > TT_KERNEL_MMA_SYNC) return fail(TT_ERR_INVALID_ARG, "unknown kernel");
   if (d.flags & ~(TT_PLAN_HOST_IO | TT_PLAN_OUT_BF16)) return fail(TT_ERR_INVALID_ARG, "unknown flag bits");
+  if (window < 0 || sinks < 0 || (sinks > 0 && window == 0))
+    return fail(TT_ERR_INVALID_ARG, "window and sinks must be >= 0, and sinks need a window");
   if (d.head_dim != 64 && d.head_dim != 128) return fail(TT_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   const int g = d.num_q_heads / d.num_kv_heads;
   if ((long long)d.block_size * g > 256) return fail(TT_ERR_UNSUPPORTED, "block_size * (Hq/Hkv) must be <= 256");
@@ -347,6 +470,8 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
 
   tt_plan_s* P = new tt_plan_s();
   P->desc = d;
+  P->window = window;
+  P->sinks = sinks;
   P->device = device;
   P->sm_count = prop.multiProcessorCount;
   P->g = g;
@@ -372,7 +497,8 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
     if (P->variant == 3 && (!tt::attn_2sm_supported(d.head_dim, g) || P->key_tile != 128)) P->variant = 0;
     // the bf16 output is written by the default kernel's epilogue (and the combine): the
     // transposed-PV and 2-SM forms, selectable for fp32 output only, fall back to it
-    if ((d.flags & TT_PLAN_OUT_BF16) && P->variant != 0) {
+    // (as are the runs of a windowed layer)
+    if (((d.flags & TT_PLAN_OUT_BF16) || window > 0) && P->variant != 0) {
       P->variant = 0;
       P->key_tile = tt::kTcgen05KeyTile;
     }
@@ -397,7 +523,9 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
     long long acc = 0;
     for (int b = 0; b <= NB; ++b) {
       pref[b] = (int)acc;
-      if (b < NB) acc += tt::ceil_div(d.block_size, P->key_tile) + tt::ceil_div(d.block_size * b, P->key_tile);
+      if (b < NB)
+        acc += tt::ceil_div(d.block_size, P->key_tile) +
+               tt::ctx_span(d.block_size * b, window, sinks, 1, P->key_tile).tiles;
     }
     if (acc > (1ll << 31) - 1) {
       delete P;
@@ -428,7 +556,7 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
   const size_t b_po = up((size_t)2 * Cmax * P->R * d.head_dim * sizeof(float));
   const size_t b_pl = up((size_t)2 * Cmax * P->R * sizeof(float));
   const size_t b_rec = up((size_t)Cmax * sizeof(tt::SplitRecord));
-  const size_t b_err = 256;
+  const size_t b_err = 256;   // the error word and, 128 bytes on, the write's ticket
   const size_t b_pref = up(pref.size() * sizeof(int));
   const size_t b_arr = up((size_t)2 * Cmax * sizeof(unsigned));
   const std::vector<long long> tab = causal_range_table(P, pref, d);
@@ -444,6 +572,7 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
   P->part_lse = reinterpret_cast<float*>(w + b_po);
   P->records = reinterpret_cast<tt::SplitRecord*>(w + b_po + b_pl);
   P->err_word = reinterpret_cast<unsigned*>(w + b_po + b_pl + b_rec);
+  P->ticket = P->err_word + 32;
   P->arr_decode = reinterpret_cast<unsigned*>(w + b_po + b_pl + b_rec + b_err + b_pref);
   P->arr_causal = P->arr_decode + Cmax;
   // The fused combine: the default tcgen05 kernel combines the cut units itself, in a
@@ -461,9 +590,14 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
     const int force = fc ? std::atoi(fc) : -1;
     const bool can = P->kernel == TT_KERNEL_TCGEN05 && P->variant == 0 && P->C > 1 && P->C <= P->sm_count;
     P->fused_combine = can && force == 1;
-    const long long unit_tiles = 1 + (long long)tt::ceil_div(d.ctx_capacity, P->key_tile);
-    // (a plan without a context capacity serves paged calls, whose lengths it cannot bound)
-    const bool short_ranges = decode_aligned && d.ctx_capacity > 0 &&
+    // tiles of a unit at most: the capacity's, or a window's (one more where its run starts in a page)
+    long long unit_tiles = 1 + (long long)tt::ceil_div(d.ctx_capacity, P->key_tile);
+    if (window > 0) {
+      const long long w = 4 + (long long)window / P->key_tile + sinks / P->key_tile;
+      unit_tiles = d.ctx_capacity > 0 ? std::min(unit_tiles, w) : w;
+    }
+    // (a plan without a context capacity or window serves paged calls, whose lengths it cannot bound)
+    const bool short_ranges = decode_aligned && (d.ctx_capacity > 0 || window > 0) &&
                               unit_tiles * d.batch * d.num_kv_heads <= 32LL * std::max(P->C_decode, 1);
     P->fused_decode = can && P->C_decode <= P->sm_count && (force == 1 || (force != 0 && short_ranges));
   }
@@ -501,6 +635,36 @@ tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_pl
   return TT_OK;
 }
 
+}  // namespace
+
+extern "C" {
+
+const char* tt_status_string(tt_status_t s) {
+  switch (s) {
+    case TT_OK: return "ok";
+    case TT_ERR_INVALID_ARG: return "invalid argument";
+    case TT_ERR_UNSUPPORTED: return "unsupported configuration";
+    case TT_ERR_CUDA: return "CUDA error";
+    case TT_ERR_DEVICE_ARG: return "device-side argument error (ctx_lens out of range)";
+    case TT_ERR_TIMEOUT: return "device-side pipeline wait timed out";
+  }
+  return "unknown status";
+}
+
+const char* tt_last_error_detail(void) { return g_detail.c_str(); }
+
+tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device, tt_plan_t* out_plan) {
+  return tt_block_attn_plan_window(desc, 0, 0, device, out_plan);
+}
+
+tt_status_t tt_block_attn_plan_window(const tt_block_attn_desc* desc, int window, int sinks, int device,
+                                      tt_plan_t* out_plan) {
+  try {
+    return make_plan(desc, window, sinks, device, out_plan);
+  } catch (const std::exception& e) {
+    return fail(TT_ERR_CUDA, std::string("host allocation: ") + e.what());
+  }
+}
 void tt_block_attn_plan_destroy(tt_plan_t plan) {
   if (!plan) return;
   DeviceGuard guard(plan->device);
@@ -525,75 +689,84 @@ tt_status_t tt_block_attn_plan_get_info(tt_plan_t plan, tt_plan_info* info) {
 
 tt_status_t tt_block_attn(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
                           const void* v_blk, const int32_t* ctx_lens, float* out, float* lse, tt_stream_t stream) {
-  if (!plan) return fail(TT_ERR_INVALID_ARG, "null plan");
-  const tt_block_attn_desc& d = plan->desc;
-  if (d.batch == 0) return TT_OK;
-  if (!q || !k_blk || !v_blk || !ctx_lens || !out) return fail(TT_ERR_INVALID_ARG, "null tensor pointer");
-  if (d.ctx_capacity > 0 && (!k_ctx || !v_ctx)) return fail(TT_ERR_INVALID_ARG, "null context pointer");
-  if (!aligned16(q) || !aligned16(k_ctx) || !aligned16(v_ctx) || !aligned16(k_blk) || !aligned16(v_blk) ||
-      !aligned16(out) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(ctx_lens) & 3u))
-    return fail(TT_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
-  DeviceGuard guard(plan->device);
-  tt::Problem p = base_problem(plan);
-  p.C = plan->C_decode;
-  p.arrivals = plan->fused_decode ? plan->arr_decode : nullptr;
-  p.mode = tt::kDecode;
-  p.NB = 1;
-  p.ctx_stride = d.ctx_capacity;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_ctx = static_cast<const __nv_bfloat16*>(k_ctx);
-  p.v_ctx = static_cast<const __nv_bfloat16*>(v_ctx);
-  p.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
-  p.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
-  p.ctx_lens = ctx_lens;
-  p.out = out;
-  p.lse = lse;
-  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  return decode_call(plan, q, CtxCache{k_ctx, v_ctx, nullptr, nullptr, false, nullptr, 0, 0, 0}, k_blk, v_blk,
+                     ctx_lens, nullptr, out, lse, stream);
 }
 
 tt_status_t tt_block_attn_paged(tt_plan_t plan, const void* q, const void* k_pages, const void* v_pages,
                                 const int32_t* page_table, int32_t num_pages, int32_t page_size,
                                 int32_t pages_per_seq, const void* k_blk, const void* v_blk, const int32_t* ctx_lens,
                                 float* out, float* lse, tt_stream_t stream) {
-  if (page_size < 16 || page_size > (1 << 16) || (page_size & (page_size - 1)))
-    return fail(TT_ERR_INVALID_ARG, "page_size must be a power of two in [16, 65536]");
-  if (num_pages < 0 || pages_per_seq < 0) return fail(TT_ERR_INVALID_ARG, "negative num_pages or pages_per_seq");
-  if (!plan) return fail(TT_ERR_INVALID_ARG, "null plan");
+  return decode_call(
+      plan, q, CtxCache{k_pages, v_pages, nullptr, nullptr, true, page_table, num_pages, page_size, pages_per_seq},
+      k_blk, v_blk, ctx_lens, nullptr, out, lse, stream);
+}
+
+tt_status_t tt_block_attn_tree(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,
+                               const void* v_blk, const int32_t* ctx_lens, const int32_t* parents, float* out,
+                               float* lse, tt_stream_t stream) {
+  if (plan && plan->desc.batch > 0 && !parents) return fail(TT_ERR_INVALID_ARG, "null parents");
+  return decode_call(plan, q, CtxCache{k_ctx, v_ctx, nullptr, nullptr, false, nullptr, 0, 0, 0}, k_blk, v_blk,
+                     ctx_lens, parents, out, lse, stream);
+}
+
+tt_status_t tt_block_attn_tree_paged(tt_plan_t plan, const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, int32_t num_pages, int32_t page_size,
+                                     int32_t pages_per_seq, const void* k_blk, const void* v_blk,
+                                     const int32_t* ctx_lens, const int32_t* parents, float* out, float* lse,
+                                     tt_stream_t stream) {
+  if (plan && plan->desc.batch > 0 && !parents) return fail(TT_ERR_INVALID_ARG, "null parents");
+  return decode_call(
+      plan, q, CtxCache{k_pages, v_pages, nullptr, nullptr, true, page_table, num_pages, page_size, pages_per_seq},
+      k_blk, v_blk, ctx_lens, parents, out, lse, stream);
+}
+
+tt_status_t tt_block_attn_mx(tt_plan_t plan, const void* q, const tt_mx_cache* cache, const void* k_blk,
+                             const void* v_blk, const int32_t* ctx_lens, const int32_t* parents, float* out,
+                             float* lse, tt_stream_t stream) {
+  if (!cache) return fail(TT_ERR_INVALID_ARG, "null cache");
+  if (!cache->k_scale || !cache->v_scale) return fail(TT_ERR_INVALID_ARG, "null cache scales");
+  return decode_call(plan, q,
+                     CtxCache{cache->k, cache->v, cache->k_scale, cache->v_scale, cache->page_table != nullptr,
+                              cache->page_table, cache->num_pages, cache->page_size, cache->pages_per_seq},
+                     k_blk, v_blk, ctx_lens, parents, out, lse, stream);
+}
+
+tt_status_t tt_kv_append_mx(tt_plan_t plan, const void* k_new, const void* v_new, int rows, const int32_t* counts,
+                            const tt_mx_cache* cache, int32_t* ctx_lens, int advance, tt_stream_t stream) {
+  tt::MxRows m;
+  const tt_status_t st = mx_rows(plan, cache, &m);
+  if (st != TT_OK) return st;
   const tt_block_attn_desc& d = plan->desc;
-  if ((long long)pages_per_seq * page_size > (1ll << 31) - 1 ||
-      (long long)num_pages * d.num_kv_heads * page_size > (1ll << 31) - 1)
-    return fail(TT_ERR_UNSUPPORTED, "page pool or page table too large (rows beyond 2^31)");
-  if (d.batch == 0) return TT_OK;
-  if (!q || !k_blk || !v_blk || !ctx_lens || !out) return fail(TT_ERR_INVALID_ARG, "null tensor pointer");
-  if (pages_per_seq > 0 && (!page_table || !k_pages || !v_pages || num_pages < 1))
-    return fail(TT_ERR_INVALID_ARG, "pages_per_seq > 0 needs a page table and non-empty pools");
-  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(k_blk) || !aligned16(v_blk) ||
-      !aligned16(out) || !aligned16(lse) || (reinterpret_cast<uintptr_t>(ctx_lens) & 3u) ||
-      (reinterpret_cast<uintptr_t>(page_table) & 3u))
+  if (rows < 0) return fail(TT_ERR_INVALID_ARG, "negative rows");
+  if (d.batch == 0 || rows == 0) return TT_OK;
+  if (!k_new || !v_new || !ctx_lens) return fail(TT_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned4(ctx_lens) || !aligned4(counts))
     return fail(TT_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
   DeviceGuard guard(plan->device);
-  tt::Problem p = base_problem(plan);
-  p.mode = tt::kDecode;
-  p.NB = 1;
-  p.variant = 0;  // the paged loads live in the default tcgen05 kernel (and the mma.sync one)
-  p.C = plan->variant == 3 ? plan->C_paged : plan->C_decode;
-  p.arrivals = plan->fused_decode ? plan->arr_decode : nullptr;
-  p.ctx_stride = pages_per_seq * page_size;
-  int shift = 0;
-  while ((1 << shift) < page_size) ++shift;
-  p.page_shift = shift;
-  p.pages_per_seq = pages_per_seq;
-  p.num_pages = num_pages;
-  p.page_table = pages_per_seq > 0 ? page_table : nullptr;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.k_ctx = static_cast<const __nv_bfloat16*>(k_pages);
-  p.v_ctx = static_cast<const __nv_bfloat16*>(v_pages);
-  p.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
-  p.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
-  p.ctx_lens = ctx_lens;
-  p.out = out;
-  p.lse = lse;
-  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e =
+      tt::launch_kv_append_mx(k_new, v_new, m, ctx_lens, counts, d.batch, rows, advance ? 1 : 0, plan->ticket,
+                              plan->err_word, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_mx launch");
+  return TT_OK;
+}
+
+tt_status_t tt_kv_read_mx(tt_plan_t plan, const tt_mx_cache* cache, const int32_t* ctx_lens, const int32_t* starts,
+                          int rows, void* k_out, void* v_out, tt_stream_t stream) {
+  tt::MxRows m;
+  const tt_status_t st = mx_rows(plan, cache, &m);
+  if (st != TT_OK) return st;
+  const tt_block_attn_desc& d = plan->desc;
+  if (rows < 0) return fail(TT_ERR_INVALID_ARG, "negative rows");
+  if (d.batch == 0 || rows == 0) return TT_OK;
+  if (!k_out || !v_out || !ctx_lens) return fail(TT_ERR_INVALID_ARG, "null tensor pointer");
+  if (!aligned16(k_out) || !aligned16(v_out) || !aligned4(ctx_lens) || !aligned4(starts))
+    return fail(TT_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
+  DeviceGuard guard(plan->device);
+  const cudaError_t e = tt::launch_kv_read_mx(m, ctx_lens, starts, d.batch, rows, k_out, v_out, plan->err_word,
+                                              reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_read_mx launch");
+  return TT_OK;
 }
 
 tt_status_t tt_block_attn_block_causal(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx,
@@ -694,6 +867,8 @@ tt_status_t tt_block_attn_block_causal_backward(tt_plan_t plan, const void* q, c
   p.D = d.head_dim;
   p.S = d.block_size;
   p.R = plan->R;
+  p.window = plan->window;
+  p.sinks = plan->sinks;
   p.N = d.seq_len;
   p.NB = d.seq_len / d.block_size;
   p.scale = plan->scale;
@@ -793,7 +968,8 @@ tt_status_t tt_block_attn_check(tt_plan_t plan, tt_stream_t stream) {
   if (w & tt::kErrTimeout) return fail(TT_ERR_TIMEOUT, "an in-kernel wait timed out");
   if (w & tt::kErrDeviceArg)
     return fail(TT_ERR_DEVICE_ARG,
-                "ctx_lens value out of range (attention: [0, ctx_capacity]; kv append: [0, ctx_capacity - block])");
+                "ctx_lens value out of range (attention: [0, ctx_capacity]; kv append: [0, ctx_capacity - rows]), a page "
+                "outside the pool, a row count or start out of range, or a tree row whose parent is not an earlier row");
   return TT_OK;
 }
 

@@ -22,6 +22,7 @@
 
 #include "errbits.h"
 #include "ptx.cuh"
+#include "sched.cuh"
 
 namespace tt {
 namespace {
@@ -111,11 +112,14 @@ __global__ void __launch_bounds__(kThreads) attn_bwd_kernel(const BwdProblem p) 
   for (int i = 0; i < D / 8; ++i) dq[i][0] = dq[i][1] = dq[i][2] = dq[i][3] = 0.f;
 
   const int L = tok0;                               // visible context of block b
-  const int n_ctx = (L + kKeys - 1) / kKeys, n_blk = (p.S + kKeys - 1) / kKeys;
+  const CtxSpan span = ctx_span(L, p.window, p.sinks, 1, kKeys);
+  const int n_ctx = span.tiles, n_blk = (p.S + kKeys - 1) / kKeys;
   for (int it = 0; it < n_ctx + n_blk; ++it) {
     const bool is_blk = it >= n_ctx;
-    const int first = is_blk ? (it - n_ctx) * kKeys : it * kKeys;
-    const int nvalid = min(kKeys, (is_blk ? p.S : L) - first);
+    const bool is_sink = it < span.sink_tiles;
+    const int first = is_blk ? (it - n_ctx) * kKeys
+                             : is_sink ? it * kKeys : span.wstart + (it - span.sink_tiles) * kKeys;
+    const int nvalid = min(kKeys, (is_blk ? p.S : is_sink ? p.sinks : L) - first);
     // ---- K, V tile (zero beyond nvalid) ----
     for (int e = tid; e < kKeys * CH; e += kThreads) {
       const int r = e / CH, ch = e - (e / CH) * CH;

@@ -9,6 +9,7 @@ namespace tt {
 
 struct BwdProblem {
   int B, Hq, Hkv, g, D, S, R, N, NB;   // N = sequence length, NB = N / S blocks
+  int window, sinks;                   // sliding window of the context (0: all of it), first tokens kept
   float scale, scale_log2;
   const __nv_bfloat16 *q, *k_ctx, *v_ctx, *k_blk, *v_blk;   // forward inputs (block-causal layouts)
   const float *out, *lse;                                     // forward outputs

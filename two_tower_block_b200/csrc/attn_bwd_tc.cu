@@ -81,7 +81,8 @@ struct Item {
   int n, h, b, m;     // sequence, KV head, block, M-tile
   int tok0;           // first token of the block
   int rows;           // valid packed rows of the M-tile
-  int tiles;          // key tiles: 1 (block keys) + ceil(S*b / 64) context tiles
+  int tiles;          // key tiles: 1 (block keys) + the context's tiles
+  int sink_tiles, wstart;   // context runs of a windowed layer (sched.cuh: CtxSpan)
 };
 
 __device__ __forceinline__ Item item_of(const BwdProblem& p, int idx, int MT) {
@@ -95,7 +96,10 @@ __device__ __forceinline__ Item item_of(const BwdProblem& p, int idx, int MT) {
   it.h = nh - it.n * p.Hkv;
   it.tok0 = it.b * p.S;
   it.rows = min(128, p.R - 128 * it.m);
-  it.tiles = 1 + ceil_div(p.S * it.b, kNK);
+  const CtxSpan s = ctx_span(it.tok0, p.window, p.sinks, 1, kNK);
+  it.sink_tiles = s.sink_tiles;
+  it.wstart = s.wstart;
+  it.tiles = 1 + s.tiles;
   return it;
 }
 
@@ -104,8 +108,11 @@ __device__ __forceinline__ void tile_range(const BwdProblem& p, const Item& it, 
   if (i == 0) {
     first = 0;
     count = p.S;
-  } else {
+  } else if (i <= it.sink_tiles) {
     first = (i - 1) * kNK;
+    count = min(kNK, p.sinks - first);
+  } else {
+    first = it.wstart + (i - 1 - it.sink_tiles) * kNK;
     count = min(kNK, it.tok0 - first);
   }
 }

@@ -7,6 +7,11 @@
 // through one online softmax -- the single joint softmax over [context ;
 // block] of the method (paperfeed.app review of arXiv 2606.26493, "The idea:
 // freeze the reader, train the writer").
+//
+// TREE: the block is a tree of drafted tokens; each row's ancestors are a bit mask in shared
+// memory, and the keys and values of absent rows are taken as zero.  MX: the context is e4m3
+// with a scale per 32 elements, converted to bf16 as a tile is brought into shared memory.
+#include "mx.cuh"
 #include "problem.h"
 #include "ptx.cuh"
 #include "walker.cuh"
@@ -17,8 +22,10 @@ namespace {
 constexpr int kRows = 64;   // packed query rows per CTA
 constexpr int kKeys = kMmaSyncKeyTile;  // keys per tile
 constexpr int kThreads = 128;
+constexpr int kMaxBlock = 256;          // S <= 256 (S * g <= 256)
+constexpr float kNoKey = -1e30f;        // reference maximum of a row that has seen no key yet
 
-template <int D>
+template <int D, bool TREE, bool MX>
 __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p) {
   constexpr int LDS = D + 8;   // padded smem row (elements): ldmatrix rows hit distinct banks
   constexpr int CH = D / 8;    // 16-byte chunks per row
@@ -28,6 +35,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
   __nv_bfloat16* sV = sK + 2 * kKeys * LDS; // [2][kKeys][LDS]
   __shared__ long long s_T, s_start, s_end;
   __shared__ Unit s_first;
+  // TREE: what each block row sees of the block, 32 rows per word, and whether it is absent
+  __shared__ uint32_t s_sees[TREE ? kMaxBlock : 1][kMaxBlock / 32];
+  __shared__ bool s_absent[TREE ? kMaxBlock : 1];
 
   const int c = blockIdx.x, rb = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -53,6 +63,18 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
 
   for (;;) {
     const Segment sg = segment_of(x, start, end, c);
+    if constexpr (TREE) {
+      for (int t = tid; t < p.S; t += kThreads) {
+        bool absent = false;
+        for (int w = 0; w < ceil_div(p.S, 64); ++w) {
+          const unsigned long long m = tree_mask(p, x.n, t, 64 * w, absent);
+          s_sees[t][2 * w] = (uint32_t)m;
+          s_sees[t][2 * w + 1] = (uint32_t)(m >> 32);
+        }
+        s_absent[t] = absent;
+      }
+      __syncthreads();
+    }
 
     // ---- Q rows [row0, row0 + 64) of this unit (rows >= R are zero) ----
     for (int i = tid; i < kRows * CH; i += kThreads) {
@@ -75,16 +97,30 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
         const __nv_bfloat16* vs = p.v_blk;
         if (valid) {
           if (tk.is_blk) {
+            if constexpr (TREE) valid = !s_absent[tk.first + r];
             const size_t off = ((size_t)(x.ns * p.S + tk.first + r) * p.Hkv + x.h) * D + ch * 8;
             ks = p.k_blk + off;
             vs = p.v_blk + off;
-          } else if (!p.page_table) {
-            const size_t off = ((size_t)(x.n * p.Hkv + x.h) * p.ctx_stride + tk.first + r) * D + ch * 8;
-            ks = p.k_ctx + off;
-            vs = p.v_ctx + off;
           } else {
-            const int row = paged_row(p, x.n, x.h, tk.first + r);  // -1: page outside the pool
+            const int row = p.page_table ? paged_row(p, x.n, x.h, tk.first + r)  // -1: page outside the pool
+                                         : (x.n * p.Hkv + x.h) * p.ctx_stride + tk.first + r;
             valid = row >= 0;  // a bad page reads as zeros
+            if constexpr (MX) {
+              uint4 kq = make_uint4(0, 0, 0, 0), vq = kq;
+              if (valid) {
+                const size_t off = (size_t)row * D + ch * 8, sc = off / kMxBlock;
+                const uint2 kw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.k_ctx) + off);
+                const uint2 vw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.v_ctx) + off);
+                const MxScale ksc = mx_scale(p.k_scale[sc]), vsc = mx_scale(p.v_scale[sc]);
+                const uint2 k0 = mx_to_bf16x4(kw.x, ksc), k1 = mx_to_bf16x4(kw.y, ksc);
+                const uint2 v0 = mx_to_bf16x4(vw.x, vsc), v1 = mx_to_bf16x4(vw.y, vsc);
+                kq = make_uint4(k0.x, k0.y, k1.x, k1.y);
+                vq = make_uint4(v0.x, v0.y, v1.x, v1.y);
+              }
+              *reinterpret_cast<uint4*>(sK + (buf * kKeys + r) * LDS + ch * 8) = kq;
+              *reinterpret_cast<uint4*>(sV + (buf * kKeys + r) * LDS + ch * 8) = vq;
+              continue;
+            }
             if (valid) {
               ks = p.k_ctx + (size_t)row * D + ch * 8;
               vs = p.v_ctx + (size_t)row * D + ch * 8;
@@ -121,7 +157,26 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
           ldmatrix_x4(a, qa[kk][0], qa[kk][1], qa[kk][2], qa[kk][3]);
         }
       }
-      const int nvalid = tile_keys(p, x, i).count;
+      const TileKeys tk = tile_keys(p, x, i);
+      const int nvalid = tk.count;
+      // rows of this thread: gq and gq + 8 of the warp's 16
+      const uint32_t* sees0 = nullptr;
+      const uint32_t* sees1 = nullptr;
+      bool none0 = false, none1 = false;
+      if constexpr (TREE) {
+        const int t0 = min(row0 + warp * 16 + gq, p.R - 1) / p.g, t1 = min(row0 + warp * 16 + gq + 8, p.R - 1) / p.g;
+        none0 = s_absent[t0];
+        none1 = s_absent[t1];
+        if (tk.is_blk) {
+          sees0 = &s_sees[t0][tk.first / 32];
+          sees1 = &s_sees[t1][tk.first / 32];
+        }
+      }
+      auto sees = [&](const uint32_t* m, bool none, int col) {
+        bool v = col < nvalid;
+        if constexpr (TREE) v = v && !none && (m == nullptr || ((m[col >> 5] >> (col & 31)) & 1u));
+        return v;
+      };
 
       // ---- S = Q K^T for 16 rows x 64 keys ----
       float s[kKeys / 8][4];
@@ -146,10 +201,10 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
 #pragma unroll
       for (int nb = 0; nb < kKeys / 8; ++nb) {
         const int col = nb * 8 + 2 * qq;
-        s[nb][0] = col < nvalid ? s[nb][0] * p.scale_log2 : -INFINITY;
-        s[nb][1] = col + 1 < nvalid ? s[nb][1] * p.scale_log2 : -INFINITY;
-        s[nb][2] = col < nvalid ? s[nb][2] * p.scale_log2 : -INFINITY;
-        s[nb][3] = col + 1 < nvalid ? s[nb][3] * p.scale_log2 : -INFINITY;
+        s[nb][0] = sees(sees0, none0, col) ? s[nb][0] * p.scale_log2 : -INFINITY;
+        s[nb][1] = sees(sees0, none0, col + 1) ? s[nb][1] * p.scale_log2 : -INFINITY;
+        s[nb][2] = sees(sees1, none1, col) ? s[nb][2] * p.scale_log2 : -INFINITY;
+        s[nb][3] = sees(sees1, none1, col + 1) ? s[nb][3] * p.scale_log2 : -INFINITY;
         mx0 = fmaxf(mx0, fmaxf(s[nb][0], s[nb][1]));
         mx1 = fmaxf(mx1, fmaxf(s[nb][2], s[nb][3]));
       }
@@ -157,7 +212,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
-      const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+      // (with a tree a row may see nothing of its first tiles: its reference stays finite)
+      const float mn0 = fmaxf(fmaxf(m0, mx0), kNoKey), mn1 = fmaxf(fmaxf(m1, mx1), kNoKey);
       const float al0 = fast_exp2(m0 - mn0), al1 = fast_exp2(m1 - mn1);  // 0 on the first tile
       m0 = mn0;
       m1 = mn1;
@@ -212,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
       const int r = row0 + warp * 16 + gq + 8 * half;
       if (r >= p.R) continue;
       const float l = half ? l1 : l0;
-      const float inv = 1.f / l;
+      const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw no key: 0 and lse = -inf
       const float lse = ((half ? m1 : m0) + __log2f(l)) * 0.6931471805599453f;
       const int t = r / p.g, j = r - (r / p.g) * p.g;
       const size_t off = out_offset(p, x, r, D);
@@ -249,16 +305,22 @@ cudaError_t launch_attn_mma_sync(const Problem& p, cudaStream_t stream) {
   const size_t smem = attn_mma_sync_smem_bytes(p.D);
   dim3 grid(p.C, (p.R + kRows - 1) / kRows);
   // The opt-in shared-memory size is set once per process (not during a graph capture).
+  using Kernel = void (*)(const Problem);
+  static const Kernel table[2][2][2] = {   // [head_dim 128][tree][mx]
+      {{attn_mma_sync_kernel<64, false, false>, attn_mma_sync_kernel<64, false, true>},
+       {attn_mma_sync_kernel<64, true, false>, attn_mma_sync_kernel<64, true, true>}},
+      {{attn_mma_sync_kernel<128, false, false>, attn_mma_sync_kernel<128, false, true>},
+       {attn_mma_sync_kernel<128, true, false>, attn_mma_sync_kernel<128, true, true>}}};
   static const bool attr_done = [] {
-    cudaFuncSetAttribute(attn_mma_sync_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)attn_mma_sync_smem_bytes(128));
-    cudaFuncSetAttribute(attn_mma_sync_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)attn_mma_sync_smem_bytes(64));
+    for (int d = 0; d < 2; ++d)
+      for (int k = 0; k < 4; ++k)
+        cudaFuncSetAttribute(table[d][k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)attn_mma_sync_smem_bytes(d ? 128 : 64));
     return true;
   }();
   (void)attr_done;
-  if (p.D == 128) attn_mma_sync_kernel<128><<<grid, kThreads, smem, stream>>>(p);
-  else attn_mma_sync_kernel<64><<<grid, kThreads, smem, stream>>>(p);
+  const Kernel k = table[p.D == 128][p.parents != nullptr][p.k_scale != nullptr];
+  k<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

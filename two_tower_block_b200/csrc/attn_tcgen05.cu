@@ -35,6 +35,13 @@
 // normalisation divides by the sum of the same bf16-rounded weights the PV
 // product used, so the result is exact up to rounding.
 //
+// VIS: tiles in which a row sees only some keys beyond a valid prefix -- a drafted tree's block
+// tiles (each row sees itself and its ancestors) and the first tile of a paged window (the load
+// starts at a page slice, before the window).  The softmax then selects by a 64-bit mask per row,
+// built by walking the row's parents (at most S steps, once per block tile); full tiles run the
+// same code as without VIS.  V rows that no row may see are cleared in shared memory, since a
+// weight of 0 does not hide an infinity or NaN in them.
+//
 // Every wait is bounded (ptx.cuh: mbar_wait); on a timeout the CTA raises the
 // error word, drains what it issued, frees TMEM and returns.
 #include <type_traits>
@@ -52,6 +59,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxRows = 256;
 constexpr int kRowBytes = 128;              // one 64-element bf16 row of a swizzled half
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
+constexpr float kNoKey = -1e30f;            // reference maximum of a row that has seen no key yet
 
 template <int D, int NK>
 struct Cfg {
@@ -146,7 +154,7 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
   }
 }
 
-template <int D, int NK>
+template <int D, int NK, bool VIS>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tcgen05_kernel(const Problem p, const __grid_constant__ TmaMaps maps) {
   using C = Cfg<D, NK>;
@@ -285,8 +293,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint32_t slot = kv_s + s * C::kSlotBytes;
         const CUtensorMap* m = tk.is_blk ? (kv ? &maps.v_blk : &maps.k_blk) : (kv ? &maps.v_ctx : &maps.k_ctx);
-        // V rows [count, round16(count)) are read by the last PV k-step: zero them.
-        const bool fix = kv == 1 && (tk.count & 15) != 0;
+        // V rows [count, round16(count)) are read by the last PV k-step: zero them (with VIS also
+        // the rows before a window and the absent rows of a tree).
+        unsigned long long zero = 0ull;
+        if constexpr (VIS) {
+          if (kv == 1) {
+            zero = span_mask(0, round16(tk.count)) & ~span_mask(tk.head, tk.count);
+            if (tk.is_blk && p.parents) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                bool absent = false;
+                if (32 * w + lane < tk.count) tree_mask(p, x.n, tk.first + 32 * w + lane, tk.first, absent);
+                zero |= (unsigned long long)__ballot_sync(0xffffffffu, absent) << (32 * w);
+              }
+            }
+          }
+        }
+        const bool fix = VIS ? zero != 0ull : kv == 1 && (tk.count & 15) != 0;
         const uint32_t bar = fix ? smem_u32(&bars->tail) : smem_u32(&bars->kv_full[s]);
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         if (nsl > 0) {
@@ -307,12 +330,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(smem_u32(&bars->tail), tail_ph, wc);
           tail_ph ^= 1;
           if (!ok) break;
-          const int r0 = tk.count, r1 = round16(tk.count);
+          const int r0 = VIS ? 0 : tk.count, r1 = round16(tk.count);
           const int n16 = (r1 - r0) * 8 * C::kHalves;  // 16-byte chunks to clear
           for (int e = lane; e < n16; e += 32) {
             const int hf = e / ((r1 - r0) * 8);
             const int rem = e - hf * (r1 - r0) * 8;
             const int row = r0 + rem / 8, ch = rem % 8;
+            if (VIS && !((zero >> row) & 1ull)) continue;
             uint4* dst = reinterpret_cast<uint4*>(smem + C::kStageOff + s * C::kSlotBytes +
                                                   hf * (NK * kRowBytes) + row * kRowBytes + ch * 16);
             *dst = make_uint4(0, 0, 0, 0);
@@ -457,18 +481,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (; ok;) {
         const Segment sg = segment_of(x, start, end, c);
         float m_ref = -INFINITY, l = 0.f;
+        // a row that a tree leaves out (or whose ancestors are left out) sees nothing
+        bool absent = false;
+        if constexpr (VIS) {
+          if (p.parents) tree_mask(p, x.n, min(r, p.R - 1) / p.g, 0, absent);
+        }
         // One tile of the softmax: its S row in registers, the row maximum in log2 units, the
         // lazy rescale of O, then P (bf16) over the S buffer.  Full tiles and the masked last
         // tile of a unit run separate code: folding them into one path would make every full
         // tile pay for the masking.
-        auto tile = [&](auto full_tag, int count, uint32_t s_addr, bool first) -> bool {
+        // (VIS: `mask` selects the keys of a tile that is not full; a row may see none of them, so
+        // its reference maximum stays finite)
+        auto tile = [&](auto full_tag, int count, unsigned long long mask, uint32_t s_addr, bool first) -> bool {
           constexpr bool kFull = decltype(full_tag)::value;
           uint32_t v[NK];
 #pragma unroll
           for (int ch = 0; ch < NK / 32; ++ch)
             if (kFull || 32 * ch < count) tmem_ld32(s_addr + 32 * ch, v + 32 * ch);
           tc_wait_ld();
-          const float mx = tile_row_max<NK, kFull>(v, count) * p.scale_log2;
+          float mx;
+          if constexpr (VIS && !kFull) mx = fmaxf(tile_row_max_masked<NK>(v, mask) * p.scale_log2, kNoKey);
+          else mx = tile_row_max<NK, kFull>(v, count) * p.scale_log2;
           if (first) {
             m_ref = mx;  // O is overwritten by the first PV of the segment
           } else {
@@ -493,11 +526,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          l += tile_exp_store<NK, kFull>(v, count, p.scale_log2, m_ref, s_addr);
+          if constexpr (VIS && !kFull) l += tile_exp_store_masked<NK>(v, count, mask, p.scale_log2, m_ref, s_addr);
+          else l += tile_exp_store<NK, kFull>(v, count, p.scale_log2, m_ref, s_addr);
           return true;
         };
         for (int i = sg.lo; i < sg.hi; ++i, ++G) {
-          const int count = tile_keys(p, x, i).count;
+          const TileKeys tk = tile_keys(p, x, i);
+          const int count = tk.count;
+          unsigned long long mask = 0ull;
+          bool full = count == NK;
+          if constexpr (VIS) {
+            const bool tree = tk.is_blk && p.parents;
+            full = full && tk.head == 0 && !tree;
+            if (!full) {
+              mask = span_mask(tk.head, count);
+              bool a = false;
+              if (tree) mask &= tree_mask(p, x.n, min(r, p.R - 1) / p.g, tk.first, a);
+            }
+          }
           const int b = G % NBUF;
           const uint32_t s_addr = s_base + b * NK;
           ok = mbar_wait(smem_u32(&bars->s_full[m][b]), (G / NBUF) & 1, wc);
@@ -506,10 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // (128-key tiles keep a single masked path: a second copy of their 128-register body
           // would not fit the register budget)
           if constexpr (NK == 128)
-            ok = tile(std::false_type{}, count, s_addr, i == sg.lo);
+            ok = tile(std::false_type{}, count, mask, s_addr, i == sg.lo);
           else
-            ok = count == NK ? tile(std::true_type{}, count, s_addr, i == sg.lo)
-                             : tile(std::false_type{}, count, s_addr, i == sg.lo);
+            ok = full ? tile(std::true_type{}, count, mask, s_addr, i == sg.lo)
+                      : tile(std::false_type{}, count, mask, s_addr, i == sg.lo);
           if (!ok) break;
           tc_wait_st();
           tc_fence_before();
@@ -520,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait(smem_u32(&bars->o_full[m]), seg_cnt & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const float inv = 1.f / l;
+        const bool none = VIS && (absent || l == 0.f);   // no visible key: 0, lse = -inf
+        const float inv = none ? 0.f : 1.f / l;
         const int rbase = m * 128 + q4 * 32;  // first packed row of this warp
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
@@ -529,6 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cc == D / 32 - 1) {
             tc_fence_before();
             mbar_arrive(smem_u32(&bars->o_empty[m]));  // O fully read: the next segment may overwrite it
+          }
+          if (VIS && none) {   // (an absent row's query may be anything: its accumulator too)
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
           // stage the 32x32 block (16-byte chunks XOR-swizzled by row) for coalesced stores
 #pragma unroll
@@ -552,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         if (r < p.R) {
-          const float lse = (m_ref + __log2f(l)) * 0.6931471805599453f;
+          const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * 0.6931471805599453f;
           if (sg.full) {
             if (p.lse) {
               const int t = r / p.g, j = r - (r / p.g) * p.g;
@@ -588,13 +639,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     fused_combine<D>(p, T, start, end, sh->first, *(volatile int*)&sh->abort_flag != 0);
 }
 
-template <int D, int NK>
+template <int D, int NK, bool VIS = false>
 void set_smem_attr() {
-  cudaFuncSetAttribute(attn_tcgen05_kernel<D, NK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaFuncSetAttribute(attn_tcgen05_kernel<D, NK, VIS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                        Cfg<D, NK>::kSmemBytes);
 }
 
-template <int D, int NK>
+template <int D, int NK, bool VIS = false>
 cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
   // a programmatic dependent of the previous kernel on the stream (its setup overlaps that
   // kernel's tail), and cooperative when the fused combine needs every CTA resident at once
@@ -610,7 +661,7 @@ cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
   attr[1].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.arrivals != nullptr ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK>, p, maps);
+  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK, VIS>, p, maps);
 }
 
 }  // namespace
@@ -623,10 +674,17 @@ cudaError_t launch_attn_tcgen05(const Problem& p, const TmaMaps& maps, cudaStrea
     set_smem_attr<128, 64>();
     set_smem_attr<64, 128>();
     set_smem_attr<64, 64>();
+    set_smem_attr<128, 64, true>();
+    set_smem_attr<64, 64, true>();
     return true;
   }();
   (void)attr_done;
   if (!tcgen05_key_tile_supported(p.key_tile)) return cudaErrorInvalidValue;
+  // trees, and paged windows whose first load may start before the window: 64-key tiles
+  if (p.parents || (p.window > 0 && p.win_align > 1)) {
+    if (p.key_tile != 64) return cudaErrorInvalidValue;
+    return p.D == 128 ? launch<128, 64, true>(p, maps, stream) : launch<64, 64, true>(p, maps, stream);
+  }
   // variant 2: head_dim 128 with 128-key tiles on the transposed-PV kernel (attn_tcgen05_pt.cu)
   if (p.D == 128 && p.key_tile == 128 && p.variant == 2) return launch_attn_pt(p, maps, stream);
   if (p.D == 128) return p.key_tile == 128 ? launch<128, 128>(p, maps, stream) : launch<128, 64>(p, maps, stream);

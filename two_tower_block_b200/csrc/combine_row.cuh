@@ -52,7 +52,8 @@ __device__ __forceinline__ void combine_row(const Problem& p, int c, const Split
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= scale_old;
     M = Mn;
-    const float w_lane = lane < n ? expf(lse_lane - M) : 0.f;
+    // (a row that saw no key in any segment has M = -inf: every weight stays 0)
+    const float w_lane = lse_lane > -INFINITY ? expf(lse_lane - M) : 0.f;
     float ws = w_lane;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
@@ -73,7 +74,7 @@ __device__ __forceinline__ void combine_row(const Problem& p, int c, const Split
       }
     }
   }
-  const float inv = 1.f / wsum;
+  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
   const int t = r / p.g, j = r - (r / p.g) * p.g;
   const size_t off = out_offset(p, x, r, D) + lane * V;
   if constexpr (V == 4) {

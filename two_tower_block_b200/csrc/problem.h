@@ -32,10 +32,20 @@ struct Problem {
   const __nv_bfloat16* v_ctx;
   const __nv_bfloat16* k_blk;
   const __nv_bfloat16* v_blk;
+  // quantised context (decode only; null k_scale: bf16): k_ctx / v_ctx then address e4m3 bytes and
+  // k_scale / v_scale one scale byte per 32 of them (mx.cuh), in the same row order
+  const uint8_t* k_scale;
+  const uint8_t* v_scale;
   const int* ctx_lens;  // decode only
   float* out;           // fp32, or bf16 when out_bf16 (the pointer then addresses bf16 elements)
   float* lse;           // may be null
   int out_bf16;         // final output rows in bf16 (round to nearest even); partials stay fp32
+  // sliding window (0: the whole context is visible): a unit sees context positions [0, sinks)
+  // and [L - window, L); its window run starts at a multiple of win_align positions
+  int window, sinks, win_align;
+  // drafted tree (decode only; null: the block is bidirectional): parents[n * S + t] is the
+  // block row that row t hangs on, -1 for the last committed token, -2 for an absent row
+  const int* parents;
   // work split
   int C;                // ranges
   int key_tile;         // keys per tile

@@ -63,6 +63,31 @@ TT_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
 // Number of tiles of a unit whose visible context has L keys.
 TT_HD int unit_tiles(int L, int key_tile) { return 1 + ceil_div(L, key_tile); }
 
+// The visible context of a unit with L committed positions on a layer with a sliding window:
+// positions [0, sinks) and [L - window, L), as two runs of tiles.  When the two meet (or the
+// layer has no window, window = 0) there is one run over [0, L).  Runs begin at a multiple of
+// `align` positions (1, or the slice of a page that one load brings in); the `head` positions
+// before the window's first one are then loaded but not visible.
+struct CtxSpan {
+  int sink_tiles;  // tiles of the first run (positions [0, sinks)); 0: a single run
+  int wstart;      // first position of the second run
+  int head;        // positions at its start that are not visible
+  int tiles;       // tiles of both runs
+};
+TT_HD CtxSpan ctx_span(int L, int window, int sinks, int align, int key_tile) {
+  CtxSpan s;
+  if (window <= 0 || (long long)L - window <= sinks) {
+    s.sink_tiles = s.wstart = s.head = 0;
+  } else {
+    const int wlo = L - window;
+    s.sink_tiles = ceil_div(sinks, key_tile);
+    s.wstart = wlo / align * align;
+    s.head = wlo - s.wstart;
+  }
+  s.tiles = s.sink_tiles + ceil_div(L - s.wstart, key_tile);
+  return s;
+}
+
 // Per-range record the attention kernel leaves for the combine: the unit that
 // is cut and begins in this range (or -1), the last range touching it, and
 // the slot choice of this range's piece.

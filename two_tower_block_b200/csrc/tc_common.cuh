@@ -91,6 +91,40 @@ __device__ __forceinline__ float tile_exp_store(const uint32_t* v, int count, fl
   return acc.x + acc.y;
 }
 
+// The same two for a tile of 64 keys of which the row sees those of `mask` (none outside [0, count)).
+template <int NK>
+__device__ __forceinline__ float tile_row_max_masked(const uint32_t* v, unsigned long long mask) {
+  static_assert(NK == 64, "one mask bit per key");
+  const uint32_t w[2] = {(uint32_t)mask, (uint32_t)(mask >> 32)};
+  float m[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < NK; ++k)
+    m[k & 1] = fmaxf(m[k & 1], ((w[k >> 5] >> (k & 31)) & 1u) ? __uint_as_float(v[k]) : -INFINITY);
+  return fmaxf(m[0], m[1]);
+}
+template <int NK>
+__device__ __forceinline__ float tile_exp_store_masked(const uint32_t* v, int count, unsigned long long mask, float c,
+                                                       float m_ref, uint32_t s_addr) {
+  const uint32_t w[2] = {(uint32_t)mask, (uint32_t)(mask >> 32)};
+  float acc = 0.f;
+#pragma unroll
+  for (int ch = 0; ch < NK / 32; ++ch) {
+    if (32 * ch >= count) break;
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int c0 = 32 * ch + 2 * k;
+      const float a = ((w[ch] >> (2 * k)) & 1u) ? fast_exp2(fmaf(__uint_as_float(v[c0]), c, -m_ref)) : 0.f;
+      const float b = ((w[ch] >> (2 * k + 1)) & 1u) ? fast_exp2(fmaf(__uint_as_float(v[c0 + 1]), c, -m_ref)) : 0.f;
+      const uint2 r = round_pair_bf16(a, b);
+      pk[k] = __byte_perm(r.x, r.y, 0x7632);
+      acc += __uint_as_float(r.x) + __uint_as_float(r.y);
+    }
+    tmem_st16(s_addr + 16 * ch, pk);
+  }
+  return acc;
+}
+
 // p = 2^(s*c - m_ref) for the tile's keys (0 beyond `count`), rounded to bf16 and
 // packed in pairs into pk[NK/2] (keys 2k, 2k+1 -> pk[k], low half first).  Returns the
 // row sum of the rounded weights.

@@ -12,6 +12,7 @@ struct Unit {
   int L;          // visible context keys
   int n, h, b;    // sequence, KV head, block index within the sequence
   int ns;         // block-sequence index n * NB + b (row block of q / k_blk / out)
+  int sink_tiles, wstart, head;  // context runs of a windowed layer (sched.cuh: CtxSpan)
   long long Tu;   // first global tile of the unit
 };
 
@@ -25,7 +26,7 @@ __device__ __forceinline__ int clamp_len(const Problem& p, int n, bool report) {
 }
 
 __device__ __forceinline__ int unit_tiles_k(const Problem& p, int L) {
-  return p.blk_tiles + ceil_div(L, p.key_tile);
+  return p.blk_tiles + ctx_span(L, p.window, p.sinks, p.win_align, p.key_tile).tiles;
 }
 
 __device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu) {
@@ -45,7 +46,11 @@ __device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu)
     x.L = p.S * x.b;
   }
   x.ns = x.n * p.NB + x.b;
-  x.tiles = unit_tiles_k(p, x.L);
+  const CtxSpan s = ctx_span(x.L, p.window, p.sinks, p.win_align, p.key_tile);
+  x.sink_tiles = s.sink_tiles;
+  x.wstart = s.wstart;
+  x.head = s.head;
+  x.tiles = p.blk_tiles + s.tiles;
   return x;
 }
 
@@ -181,24 +186,61 @@ __device__ __forceinline__ void store_out2(const Problem& p, size_t off, float2 
   else *reinterpret_cast<float2*>(p.out + off) = v;
 }
 
-// Keys of unit-local tile i: block keys for i < blk_tiles, context keys after.
+// Keys of unit-local tile i: block keys for i < blk_tiles, context keys after (the sinks'
+// tiles first on a windowed layer).
 struct TileKeys {
   bool is_blk;
   int first;   // first key index within its source (block position or context position)
-  int count;   // valid keys in the tile (>= 1)
+  int count;   // keys of the tile that are loaded (>= 1)
+  int head;    // of those, the first ones that are not visible (paged windows only)
 };
 __device__ __forceinline__ TileKeys tile_keys(const Problem& p, const Unit& x, int i) {
   TileKeys k;
+  k.head = 0;
   if (i < p.blk_tiles) {
     k.is_blk = true;
     k.first = i * p.key_tile;
     k.count = min(p.S - k.first, p.key_tile);
   } else {
     k.is_blk = false;
-    k.first = (i - p.blk_tiles) * p.key_tile;
-    k.count = min(x.L - k.first, p.key_tile);
+    const int j = i - p.blk_tiles - x.sink_tiles;
+    if (j < 0) {
+      k.first = (i - p.blk_tiles) * p.key_tile;
+      k.count = min(p.sinks - k.first, p.key_tile);
+    } else {
+      k.first = x.wstart + j * p.key_tile;
+      k.count = min(x.L - k.first, p.key_tile);
+      if (j == 0) k.head = x.head;
+    }
   }
   return k;
+}
+
+// Drafted trees: the block rows of tile [first, first + 64) that row t of sequence n sees
+// (itself and its ancestors) as a bit mask; `absent` when the row or one of its ancestors is
+// not there (such a row sees nothing at all).  Parents come before their children, so the walk
+// ends; an entry that breaks this or is below -2 is flagged and its row taken as absent.
+__device__ __forceinline__ unsigned long long tree_mask(const Problem& p, int n, int t, int first, bool& absent) {
+  const int* par = p.parents + (size_t)n * p.S;
+  unsigned long long m = 0ull;
+  absent = false;
+  int u = t;
+  while (u >= 0) {
+    if (u >= first && u < first + 64) m |= 1ull << (u - first);
+    const int up = __ldg(par + u);
+    if (up >= u || up < -2) raise_error(p.err_word, kErrDeviceArg);
+    if (up >= u || up < -1) {
+      absent = true;
+      return 0ull;
+    }
+    u = up;
+  }
+  return m;
+}
+// The visible keys of a loaded tile without a tree: [head, count).
+__device__ __forceinline__ unsigned long long span_mask(int head, int count) {
+  const unsigned long long upto = count >= 64 ? ~0ull : (1ull << count) - 1;
+  return upto & (~0ull << head);
 }
 
 // Pool row (of the [num_pages * Hkv * page_size] rows of k_ctx / v_ctx) holding context

@@ -14,7 +14,7 @@ from dataclasses import dataclass
 
 import torch
 
-__all__ = ["TTError", "Plan", "lib", "library_path", "block_attn", "block_attn_block_causal", "confidence_unmask",
+__all__ = ["TTError", "Plan", "lib", "library_path", "block_attn", "block_attn_block_causal", "confidence_unmask", "MxCache",
            "selftest_wait_timeout", "work_split", "KERNEL_AUTO", "KERNEL_TCGEN05", "KERNEL_MMA_SYNC",
            "TT_OK", "TT_ERR_INVALID_ARG", "TT_ERR_UNSUPPORTED", "TT_ERR_CUDA", "TT_ERR_DEVICE_ARG",
            "TT_ERR_TIMEOUT", "EXPORTED_SYMBOLS"]
@@ -34,7 +34,8 @@ EXPORTED_SYMBOLS = [
     "tt_block_attn_profile_read", "tt_selftest_wait_timeout", "tt_debug_work_split", "tt_status_string",
     "tt_last_error_detail", "tt_block_attn_noalloc", "tt_selftest_exp2", "tt_kv_append",
     "tt_block_attn_block_causal_backward", "tt_confidence_unmask", "tt_block_attn_paged",
-    "tt_debug_causal_split",
+    "tt_debug_causal_split", "tt_block_attn_plan_window", "tt_block_attn_tree", "tt_block_attn_tree_paged",
+    "tt_kv_append_mx", "tt_kv_read_mx", "tt_block_attn_mx",
 ]
 
 
@@ -49,6 +50,12 @@ class PlanInfo(ctypes.Structure):
     _fields_ = [("kernel", ctypes.c_int), ("num_ctas", ctypes.c_int), ("key_tile", ctypes.c_int),
                 ("rows_per_unit", ctypes.c_int), ("workspace_bytes", ctypes.c_size_t),
                 ("sm_count", ctypes.c_int), ("variant", ctypes.c_int), ("fused_combine", ctypes.c_int)]
+
+
+class MxCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("pages_per_seq", ctypes.c_int32)]
 
 
 _lib = None
@@ -76,6 +83,13 @@ def lib() -> ctypes.CDLL:
     L.tt_block_attn_profile_read.argtypes = [vp, i, ip, ctypes.POINTER(ctypes.c_double)]
     L.tt_selftest_wait_timeout.argtypes = [i, i, vp]
     L.tt_debug_work_split.argtypes = [i, ip, i, ctypes.POINTER(ctypes.c_longlong), ip, ip]
+    L.tt_block_attn_plan_window.argtypes = [ctypes.POINTER(Desc), i, i, i, ctypes.POINTER(vp)]
+    L.tt_block_attn_tree.argtypes = [vp] * 11
+    L.tt_block_attn_tree_paged.argtypes = [vp, vp, vp, vp, vp, i, i, i] + [vp] * 7
+    cp = ctypes.POINTER(MxCacheDesc)
+    L.tt_kv_append_mx.argtypes = [vp, vp, vp, i, vp, cp, vp, i, vp]
+    L.tt_kv_read_mx.argtypes = [vp, cp, vp, vp, i, vp, vp, vp]
+    L.tt_block_attn_mx.argtypes = [vp, vp, cp, vp, vp, vp, vp, vp, vp, vp]
     L.tt_debug_causal_split.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
     L.tt_block_attn_noalloc.argtypes = [ctypes.POINTER(Desc)] + [vp] * 10
     L.tt_selftest_exp2.argtypes = [i, vp, vp, i]
@@ -165,13 +179,64 @@ class Shape:
     seq_len: int = 0
 
 
+class MxCache:
+    """A context cache in microscaled e4m3 (the header's tt_mx_cache): values k, v in any 1-byte type
+    and scale bytes k_scale, v_scale with the last dimension D / 32.  Slabs [B, Hkv, Lcap, D], or with
+    `page_table` [B, pages_per_seq] pools [num_pages, Hkv, P, D].  Holds the tensors it describes."""
+
+    def __init__(self, k, k_scale, v, v_scale, page_table=None):
+        if k.dim() != 4 or k.shape[3] % 32:
+            raise ValueError(f"k: shape {tuple(k.shape)}, expected four dimensions, the last a multiple of 32")
+        self.k, self.k_scale, self.v, self.v_scale, self.page_table = k, k_scale, v, v_scale, page_table
+        self.shape = tuple(k.shape)
+        n = k.numel()
+        items = [(k, "k", n, "u8"), (v, "v", n, "u8"), (k_scale, "k_scale", n // 32, "u8"),
+                 (v_scale, "v_scale", n // 32, "u8")]
+        num_pages = page_size = pages_per_seq = 0
+        if page_table is not None:
+            if page_table.dim() != 2:
+                raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [B, pages_per_seq]")
+            num_pages, page_size, pages_per_seq = k.shape[0], k.shape[2], page_table.shape[1]
+            items.append((page_table, "page_table", page_table.numel(), "i32"))
+        self.device = k.device
+        _args(k.device.index if k.is_cuda else None, *items)
+        self._d = MxCacheDesc(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), num_pages, page_size,
+                              pages_per_seq)
+        self._ref = ctypes.byref(self._d)
+
+    @classmethod
+    def empty(cls, rows_of, kv_heads, positions, head_dim, device="cuda", page_table=None):
+        """A new cache of zeros: `rows_of` sequences of `positions` rows, or (with a page table) that
+        many pages of `positions` rows."""
+        shape = (rows_of, kv_heads, positions, head_dim)
+        new = [torch.zeros(shape[:3] + (head_dim // w,), dtype=t, device=device)
+               for w, t in ((1, torch.float8_e4m3fn), (32, torch.uint8)) for _ in range(2)]
+        return cls(new[0], new[2], new[1], new[3], page_table=page_table)
+
+    def _fits(self, plan):
+        """The cache's layout against a plan's shape and device."""
+        s = plan.shape
+        if self.device.type != "cuda" or self.device.index != plan.device:
+            raise ValueError(f"cache: expected on cuda:{plan.device}, got {self.device}")
+        if self.page_table is None:
+            want = (s.batch, s.kv_heads, s.ctx_capacity, s.head_dim)
+            if self.shape != want:
+                raise ValueError(f"cache: shape {self.shape}, expected {want}")
+        elif self.shape[1] != s.kv_heads or self.shape[3] != s.head_dim or self.page_table.shape[0] != s.batch:
+            raise ValueError(f"cache: pages {self.shape} with a table {tuple(self.page_table.shape)}, expected "
+                             f"[num_pages, {s.kv_heads}, P, {s.head_dim}] and [{s.batch}, pages_per_seq]")
+        return self._ref
+
+
 class Plan:
-    """Owns a tt_plan_t (device scratch, work split) for one shape on one device."""
+    """Owns a tt_plan_t (device scratch, work split) for one shape on one device.  With ``window`` every
+    attention call sees, of a block's context, the last ``window`` positions and the first ``sinks``."""
 
     out_dtype = torch.float32   # torch.bfloat16 for a plan made with out_bf16=True
 
     def __init__(self, batch, q_heads, kv_heads, head_dim, block, ctx_capacity=0, seq_len=0, scale=0.0,
-                 kernel=KERNEL_AUTO, num_ctas=0, host_io=False, wait_timeout_us=0, device=None, out_bf16=False):
+                 kernel=KERNEL_AUTO, num_ctas=0, host_io=False, wait_timeout_us=0, device=None, out_bf16=False,
+                 window=0, sinks=0):
         if device is None:
             device = torch.cuda.current_device()
         self.shape = Shape(batch, q_heads, kv_heads, head_dim, block, ctx_capacity, seq_len)
@@ -180,7 +245,8 @@ class Plan:
         d = Desc(batch, q_heads, kv_heads, head_dim, block, ctx_capacity, seq_len, float(scale), kernel,
                  num_ctas, (PLAN_HOST_IO if host_io else 0) | (PLAN_OUT_BF16 if out_bf16 else 0), wait_timeout_us)
         h = ctypes.c_void_p()
-        _check(lib().tt_block_attn_plan(ctypes.byref(d), self.device, ctypes.byref(h)), "tt_block_attn_plan")
+        _check(lib().tt_block_attn_plan_window(ctypes.byref(d), int(window), int(sinks), self.device,
+                                               ctypes.byref(h)), "tt_block_attn_plan")
         self._h = h
 
     def close(self):
@@ -222,19 +288,17 @@ class Plan:
                 (ctx_lens, "ctx_lens", s.batch, "i32"), (out, "out", nq, self._out_kind()),
                 (lse, "lse", s.batch * s.q_heads * s.block, "f32")]
 
-    def _out_kind(self):
-        return "bf16" if self.out_dtype == torch.bfloat16 else "f32"
-
-    def block_attn_paged(self, q, k_pages, v_pages, page_table, k_blk, v_blk, ctx_lens, out=None, lse=None,
-                         stream=None, want_lse=False):
-        """Decode over a paged context cache: k_pages / v_pages [num_pages, Hkv, P, D] bf16
-        pools, page_table [B, pages_per_seq] int32 (device); P = k_pages.shape[2].  With no
-        context at all, the pools and the table may be None."""
+    def _decode_outputs(self, q, out, lse, want_lse):
         s = self.shape
         if out is None:
             out = torch.empty((s.batch, s.block, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
         if lse is None and want_lse:
             lse = torch.empty((s.batch, s.q_heads, s.block), dtype=torch.float32, device=q.device)
+        return out, lse
+
+    def _page_items(self, k_pages, v_pages, page_table):
+        """(num_pages, page_size, pages_per_seq, items to check) of a paged context."""
+        s = self.shape
         if k_pages is None:
             num_pages, page_size = 0, 16      # no pool: valid only without context (the library checks)
         else:
@@ -248,14 +312,99 @@ class Plan:
             if page_table.dim() != 2 or page_table.shape[0] != s.batch:
                 raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [{s.batch}, pages_per_seq]")
             pages_per_seq = page_table.shape[1]
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
-              (k_pages, "k_pages", pool_numel, "bf16"), (v_pages, "v_pages", pool_numel, "bf16"),
-              (page_table, "page_table", s.batch * pages_per_seq, "i32"))
+        return int(num_pages), int(page_size), int(pages_per_seq), [
+            (k_pages, "k_pages", pool_numel, "bf16"), (v_pages, "v_pages", pool_numel, "bf16"),
+            (page_table, "page_table", s.batch * pages_per_seq, "i32")]
+
+    def _out_kind(self):
+        return "bf16" if self.out_dtype == torch.bfloat16 else "f32"
+
+    def block_attn_paged(self, q, k_pages, v_pages, page_table, k_blk, v_blk, ctx_lens, out=None, lse=None,
+                         stream=None, want_lse=False):
+        """Decode over a paged context cache: k_pages / v_pages [num_pages, Hkv, P, D] bf16
+        pools, page_table [B, pages_per_seq] int32 (device); P = k_pages.shape[2].  With no
+        context at all, the pools and the table may be None."""
+        s = self.shape
+        if out is None:
+            out = torch.empty((s.batch, s.block, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
+        if lse is None and want_lse:
+            lse = torch.empty((s.batch, s.q_heads, s.block), dtype=torch.float32, device=q.device)
+        num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
+        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse), *items)
         _check(lib().tt_block_attn_paged(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
                                          int(num_pages), int(page_size), int(pages_per_seq), _ptr(k_blk),
                                          _ptr(v_blk), _ptr(ctx_lens), _ptr(out), _ptr(lse), _stream(stream)),
                "tt_block_attn_paged")
         return (out, lse) if want_lse or lse is not None else out
+
+    def block_attn_tree(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, parents, out=None, lse=None, stream=None,
+                        want_lse=False):
+        """Decode whose block is a tree of drafted tokens: parents [B, S] int32 (-1: hangs on the last
+        committed token, -2: absent).  Otherwise as block_attn."""
+        s = self.shape
+        out, lse = self._decode_outputs(q, out, lse, want_lse)
+        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
+        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
+              (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16"),
+              (parents, "parents", s.batch * s.block, "i32"))
+        _check(lib().tt_block_attn_tree(self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk),
+                                        _ptr(ctx_lens), _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)),
+               "tt_block_attn_tree")
+        return (out, lse) if want_lse or lse is not None else out
+
+    def block_attn_tree_paged(self, q, k_pages, v_pages, page_table, k_blk, v_blk, ctx_lens, parents, out=None,
+                              lse=None, stream=None, want_lse=False):
+        """block_attn_tree over a paged context cache (pages as block_attn_paged)."""
+        s = self.shape
+        out, lse = self._decode_outputs(q, out, lse, want_lse)
+        num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
+        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse), *items,
+              (parents, "parents", s.batch * s.block, "i32"))
+        _check(lib().tt_block_attn_tree_paged(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                                              num_pages, page_size, pages_per_seq, _ptr(k_blk), _ptr(v_blk),
+                                              _ptr(ctx_lens), _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)),
+               "tt_block_attn_tree_paged")
+        return (out, lse) if want_lse or lse is not None else out
+
+    # --- quantised context cache ---------------------------------------------
+    def block_attn_mx(self, q, cache, k_blk, v_blk, ctx_lens, parents=None, out=None, lse=None, stream=None,
+                      want_lse=False):
+        """Decode over a quantised context cache (MxCache); with ``parents`` the block is a drafted tree."""
+        s = self.shape
+        out, lse = self._decode_outputs(q, out, lse, want_lse)
+        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
+              (parents, "parents", s.batch * s.block, "i32"))
+        _check(lib().tt_block_attn_mx(self._h, _ptr(q), cache._fits(self), _ptr(k_blk), _ptr(v_blk), _ptr(ctx_lens),
+                                      _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)), "tt_block_attn_mx")
+        return (out, lse) if want_lse or lse is not None else out
+
+    def kv_append_mx(self, k_new, v_new, cache, ctx_lens, counts=None, advance=True, stream=None):
+        """Quantise k_new/v_new [B, rows, Hkv, D] into the cache at [L_n, L_n + counts[n]) (all rows
+        without ``counts``) and advance ctx_lens (device int32) when ``advance``."""
+        s = self.shape
+        if k_new.dim() != 4 or k_new.shape[0] != s.batch or k_new.shape[2:] != (s.kv_heads, s.head_dim):
+            raise ValueError(f"k_new: shape {tuple(k_new.shape)}, expected [{s.batch}, rows, {s.kv_heads}, "
+                             f"{s.head_dim}]")
+        n = k_new.numel()
+        _args(self.device, (k_new, "k_new", n, "bf16"), (v_new, "v_new", n, "bf16"),
+              (ctx_lens, "ctx_lens", s.batch, "i32"), (counts, "counts", s.batch, "i32"))
+        _check(lib().tt_kv_append_mx(self._h, _ptr(k_new), _ptr(v_new), k_new.shape[1], _ptr(counts),
+                                     cache._fits(self), _ptr(ctx_lens), int(bool(advance)), _stream(stream)),
+               "tt_kv_append_mx")
+
+    def kv_read_mx(self, cache, ctx_lens, starts, k_out, v_out, stream=None):
+        """Positions [starts[n], starts[n] + rows) below ctx_lens[n] back as bf16 into k_out/v_out
+        [B, Hkv, rows, D] (``starts`` None: 0); other rows are left as they were."""
+        s = self.shape
+        if k_out.dim() != 4 or k_out.shape[:2] != (s.batch, s.kv_heads) or k_out.shape[3] != s.head_dim:
+            raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [{s.batch}, {s.kv_heads}, rows, "
+                             f"{s.head_dim}]")
+        n = k_out.numel()
+        _args(self.device, (k_out, "k_out", n, "bf16"), (v_out, "v_out", n, "bf16"),
+              (ctx_lens, "ctx_lens", s.batch, "i32"), (starts, "starts", s.batch, "i32"))
+        _check(lib().tt_kv_read_mx(self._h, cache._fits(self), _ptr(ctx_lens), _ptr(starts), k_out.shape[2],
+                                   _ptr(k_out), _ptr(v_out), _stream(stream)), "tt_kv_read_mx")
+        return k_out, v_out
 
     def block_attn_host(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out, lse=None, stream=None):
         """Host (ideally pinned) CPU tensors in and out; copies happen inside the library."""
