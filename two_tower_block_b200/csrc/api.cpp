@@ -187,9 +187,7 @@ tt::Problem base_problem(tt_plan_t plan) {
 tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s) {
   cudaError_t e;
   prof_mark(plan, 0, s, true);
-  if (p.k_scale) {
-    e = tt::launch_attn_mma_sync(p, s);
-  } else if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 3) {
+  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 3) {
     e = tt::launch_attn_2sm(p, s);
   } else if (plan->kernel == TT_KERNEL_TCGEN05) {
     tt::TmaMaps maps;
@@ -212,6 +210,10 @@ tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s) {
           !encode_bf16(&maps.v_blk, p.v_blk, 3, dims, str, box))
         return fail(TT_ERR_CUDA, "tensor map (block kv) encode failed");
     }
+    if (p.k_scale) {
+      maps.k_ctx = maps.k_blk;  // never read: a quantised context is not loaded through tensor maps
+      maps.v_ctx = maps.v_blk;
+    } else
     // paged: k_ctx / v_ctx are pools viewed as [num_pages*Hkv*page_size rows][D]; box =
     // min(page_size, key_tile) rows x 64 dims (one page's slice of a tile)
     if (p.page_table && (uint64_t)p.num_pages * p.Hkv * p.ctx_stride > 0) {
@@ -377,11 +379,10 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
     p.num_pages = c.num_pages;
     p.page_table = c.pages_per_seq > 0 ? c.table : nullptr;
     // the tcgen05 kernel loads whole slices of a page: its window run starts at one
-    if (plan->kernel == TT_KERNEL_TCGEN05 && !mx) p.win_align = std::min(c.page_size, p.key_tile);
+    if (plan->kernel == TT_KERNEL_TCGEN05) p.win_align = std::min(c.page_size, p.key_tile);
   } else {
     p.ctx_stride = d.ctx_capacity;
   }
-  if (mx) p.arrivals = nullptr;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_ctx = static_cast<const __nv_bfloat16*>(c.k);
   p.v_ctx = static_cast<const __nv_bfloat16*>(c.v);

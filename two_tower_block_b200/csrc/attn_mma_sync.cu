@@ -111,11 +111,8 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
                 const size_t off = (size_t)row * D + ch * 8, sc = off / kMxBlock;
                 const uint2 kw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.k_ctx) + off);
                 const uint2 vw = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(p.v_ctx) + off);
-                const MxScale ksc = mx_scale(p.k_scale[sc]), vsc = mx_scale(p.v_scale[sc]);
-                const uint2 k0 = mx_to_bf16x4(kw.x, ksc), k1 = mx_to_bf16x4(kw.y, ksc);
-                const uint2 v0 = mx_to_bf16x4(vw.x, vsc), v1 = mx_to_bf16x4(vw.y, vsc);
-                kq = make_uint4(k0.x, k0.y, k1.x, k1.y);
-                vq = make_uint4(v0.x, v0.y, v1.x, v1.y);
+                kq = mx_to_bf16x8(kw, p.k_scale[sc]);
+                vq = mx_to_bf16x8(vw, p.v_scale[sc]);
               }
               *reinterpret_cast<uint4*>(sK + (buf * kKeys + r) * LDS + ch * 8) = kq;
               *reinterpret_cast<uint4*>(sV + (buf * kKeys + r) * LDS + ch * 8) = vq;

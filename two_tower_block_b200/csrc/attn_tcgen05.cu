@@ -42,11 +42,16 @@
 // same code as without VIS.  V rows that no row may see are cleared in shared memory, since a
 // weight of 0 does not hide an infinity or NaN in them.
 //
+// MX: the context is e4m3 with a scale byte per 32 elements.  Four more warps (12..15) bring the
+// context tiles in as they are and write them, as bf16, into the same ring (convert_tiles); the
+// producer warps keep Q and the block's own tiles.
+//
 // Every wait is bounded (ptx.cuh: mbar_wait); on a timeout the CTA raises the
 // error word, drains what it issued, frees TMEM and returns.
 #include <type_traits>
 
 #include "combine_row.cuh"
+#include "mx.cuh"
 #include "problem.h"
 #include "ptx.cuh"
 #include "tc_common.cuh"
@@ -55,30 +60,40 @@
 namespace tt {
 namespace {
 
-constexpr int kThreads = 384;
 constexpr int kMaxRows = 256;
 constexpr int kRowBytes = 128;              // one 64-element bf16 row of a swizzled half
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr float kNoKey = -1e30f;            // reference maximum of a row that has seen no key yet
 
-template <int D, int NK>
+template <int D, int NK, bool MX = false>
 struct Cfg {
+  static constexpr int kThreads = MX ? 512 : 384;
   static constexpr int kHalves = D / 64;
   static constexpr int kBufs = 128 / NK;                       // S buffers per M-tile
   static constexpr int kSlotBytes = NK * kRowBytes * kHalves;  // one K or V tile
-  static constexpr int kStages = (128 * 1024) / kSlotBytes;    // 128 KB ring
+  static constexpr int kStages = (MX ? 64 : 128) * 1024 / kSlotBytes;  // the ring: 128 KB, or 64 KB beside raw tiles
   static constexpr int kQBytes = kMaxRows * kRowBytes * kHalves;
   static constexpr int kStageOff = kQBytes;
   static constexpr int kEpiOff = kStageOff + kStages * kSlotBytes;
   static constexpr int kEpiBytes = 8 * 32 * 32 * 4;  // 8 softmax warps x 32 rows x 32 fp32
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
-  static constexpr int kSmemBytes = kBarOff + 512 + 1024;  // barriers/flags + alignment slack
-  // Register split (launch: 168 per thread = 65536 / 384 rounded down to 8): the
-  // 128-key variant keeps a full 128-score row per softmax thread.
-  static constexpr bool kSplitRegs = NK == 128;
-  static constexpr int kCtrlRegs = 80, kSoftmaxRegs = 200;
-  static_assert(4 * 32 * kCtrlRegs + 8 * 32 * kSoftmaxRegs <= kThreads * 168, "register split");
-  static_assert(kStages <= 16, "ring too deep");
+  static constexpr int kBarBytes = 896;
+  // MX: each converter warp's ring of raw pieces, 32 rows of e4m3, their scale bytes and a row mask
+  static constexpr int kRawOff = kBarOff + kBarBytes;
+  static constexpr int kRawScale = 32 * D;             // byte offsets within a piece
+  static constexpr int kRawMask = kRawScale + 32 * (D / kMxBlock) + 12;
+  static constexpr int kRawBytes = 32 * D + (D == 128 ? 160 : 96);
+  static constexpr int kRaw = MX ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kSmemBytes = kRawOff + 4 * kRaw * kRawBytes + 1024;  // + alignment slack
+  // Register split: the 128-key variant keeps a full 128-score row per softmax thread (launch: 168
+  // per thread = 65536 / 384 rounded down to 8); with converter warps the launch gives 128 and
+  // the softmax takes its 176 from the others.
+  static constexpr bool kSplitRegs = NK == 128 || MX;
+  static constexpr int kCtrlRegs = 80, kConvRegs = 80, kSoftmaxRegs = MX ? 176 : 200;
+  static_assert(4 * 32 * (kCtrlRegs + (MX ? kConvRegs : 0)) + 8 * 32 * kSoftmaxRegs <= kThreads * (MX ? 128 : 168),
+                "register split");
+  static_assert(kStages <= 16 && kRaw <= 6, "ring too deep");
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
 struct Bars {
@@ -86,6 +101,8 @@ struct Bars {
   uint64_t s_full[2][2], p_full[2][2];  // [M-tile][S buffer]
   uint64_t pv_done[2], o_full[2], o_empty[2];
   uint64_t kv_full[16], kv_empty[16];
+  uint64_t blk_go[16];      // MX: this slot is free for a block tile
+  uint64_t raw_full[4][6];  // MX: [converter warp][piece]
 };
 
 struct Shared {
@@ -94,7 +111,7 @@ struct Shared {
   long long T, start, end;
   Unit first;
 };
-static_assert(sizeof(Bars) + sizeof(Shared) <= 512, "barrier block overflows its shared-memory slot");
+static_assert(sizeof(Bars) + sizeof(Shared) <= 896, "barrier block overflows its shared-memory slot");
 
 // Fused split combine (cooperative launch only: every CTA is resident).  Once its segments and
 // partials are written, each CTA adds one to its range's arrival count; every range does so
@@ -105,7 +122,7 @@ static_assert(sizeof(Bars) + sizeof(Shared) <= 512, "barrier block overflows its
 // unit's n ranges, one warp per row.  No CTA waits for ranges outside its units.  The waits
 // are bounded; a CTA that gave up (or whose pipeline aborted) combines nothing and the error
 // word says so.
-template <int D>
+template <int D, int THREADS, int PARTS>   // PARTS: partials of a row in flight
 __device__ __forceinline__ void fused_combine(const Problem& p, long long T, long long start, long long end,
                                               const Unit& first, bool aborted) {
   __shared__ unsigned s_k;
@@ -150,15 +167,171 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const int n = c1 - c0 + 1, i = c - c0;
     const SplitRecord rec{x.u, c1, x.Tu == range_start_tab(tab, T, Ce, c0) ? 0 : 1, 0};
     const int r0 = (int)((long long)i * p.R / n), r1 = (int)((long long)(i + 1) * p.R / n);
-    for (int r = r0 + warp; r < r1; r += kThreads / 32) combine_row<D, 16>(p, c0, rec, r, lane);
+    for (int r = r0 + warp; r < r1; r += THREADS / 32) combine_row<D, PARTS>(p, c0, rec, r, lane);
   }
 }
 
-template <int D, int NK, bool VIS>
-__global__ void __launch_bounds__(kThreads, 1)
+// MX: the context tiles, brought in as e4m3 and converted to bf16 in the ring's K or V half.  Converter
+// warp w of 0..3 takes rows [32 (w & 1), 32 (w & 1) + 32) of every K (w < 2) or V tile of the CTA's
+// range, in the producers' order.  It loads its own pieces, so no other warp has to wait for them: the
+// rows by untiled bulk copies (rows of a cache or page lie one after another), the scale bytes by
+// four-byte asynchronous copies, both counted by the piece's barrier, kRaw pieces ahead.  Then 16
+// bytes at a time become 32 bytes of the swizzled tile; rows that are not visible (or whose page
+// lies outside the pool) become zeros, so P V meets no other row.  In each quarter of a
+// warp, four lanes work on one 64-element half of a row and four on the other half of the next
+// row, which keeps both the loads and the swizzled stores free of bank conflicts.
+template <int D, int NK>
+__device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
+                                              const WaitCtx& wc, int c, int w, int lane) {
+  using C = Cfg<D, NK, true>;
+  constexpr int H = C::kStages / 2, kRowScale = D / kMxBlock;
+  const int kv = w >> 1, first_row = 32 * (w & 1);
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? p.v_ctx : p.k_ctx);
+  const uint8_t* scales = kv ? p.v_scale : p.k_scale;
+  uint8_t* raw = smem + C::kRawOff + w * C::kRaw * C::kRawBytes;
+  const long long start = sh->start, end = sh->end;
+
+  // the CTA's context tiles in order, ahead of the conversion
+  struct Cursor {
+    Unit x;
+    Segment sg;
+    int i;
+    bool done;
+  };
+  auto settle = [&](Cursor& q) {
+    for (;;) {
+      q.i = max(q.i, p.blk_tiles);
+      if (q.i < q.sg.hi) return;
+      if (q.sg.last) {
+        q.done = true;
+        return;
+      }
+      q.x = make_unit(p, q.x.u + 1, q.x.Tu + q.x.tiles);
+      q.sg = segment_of(q.x, start, end, c);
+      q.i = q.sg.lo;
+    }
+  };
+  auto advance = [&](Cursor& q) {
+    ++q.i;
+    settle(q);
+  };
+  auto load = [&](const Cursor& q, uint32_t piece) {
+    uint8_t* dst = raw + piece * C::kRawBytes;
+    const uint32_t bar = smem_u32(&bars->raw_full[w][piece]);
+    const TileKeys tk = tile_keys(p, q.x, q.i);
+    const int n = min(max(tk.count - first_row, 0), 32);     // rows of this piece
+    const int psub = p.page_table ? min(1 << p.page_shift, 32) : 32;   // rows that lie together
+    const int mine = min(max(n - lane * psub, 0), psub);     // of them, lane's slice
+    int row = 0;
+    if (mine > 0) {
+      const int pos = tk.first + first_row + lane * psub;
+      row = p.page_table ? paged_row(p, q.x.n, q.x.h, pos) : (q.x.n * p.Hkv + q.x.h) * p.ctx_stride + pos;
+    }
+    const bool there = mine > 0 && row >= 0;
+    const uint32_t rows = __reduce_add_sync(0xffffffffu, there ? mine : 0);
+    const uint32_t bits = __reduce_or_sync(0xffffffffu, there ? (0xffffffffu >> (32 - mine)) << (lane * psub) : 0u);
+    if (lane == 0) {
+      const int head = min(max(tk.head - first_row, 0), 32);
+      *reinterpret_cast<uint32_t*>(dst + C::kRawMask) = head < 32 ? bits & (0xffffffffu << head) : 0u;
+      mbar_arrive_expect_tx(bar, rows * D);
+    }
+    __syncwarp();
+    if (there) bulk_load(smem_u32(dst) + lane * psub * D, src + (size_t)row * D, mine * D, bar);
+    // scale bytes in words of four; of a contiguous head_dim 64 cache the first word may hold the
+    // row in front of the piece's first (the converter skips it), the last word may be half a one
+    const int odd = D == 64 ? __shfl_sync(0xffffffffu, row, 0) & 1 : 0;
+#pragma unroll
+    for (int e = 0; e < (D == 64 ? 17 : 32); e += 32) {
+      const int r = (e + lane) * 4 / kRowScale - odd;        // first row of the word
+      const int s = p.page_table ? max(r, 0) / psub : 0;
+      const int row_s = __shfl_sync(0xffffffffu, row, s & 31);
+      const bool ok_s = __shfl_sync(0xffffffffu, there, s & 31);
+      if (r < n && ok_s)
+        cp_async_4(smem_u32(dst) + C::kRawScale + (e + lane) * 4, scales + ((size_t)(row_s - s * psub) + r) * kRowScale,
+                   min(4, (n - r) * kRowScale));
+    }
+    cp_async_mbar_arrive(bar);
+  };
+
+  Cursor a;
+  a.x = sh->first;
+  a.sg = segment_of(a.x, start, end, c);
+  a.i = a.sg.lo;
+  a.done = false;
+  settle(a);
+  uint32_t issued = 0, k = 0, t = 0;   // pieces loaded, pieces converted, tiles of the CTA passed
+  for (; issued < (uint32_t)C::kRaw && !a.done; ++issued, advance(a)) load(a, issued);
+  bool ok = true;
+  Unit x = sh->first;
+  const int k4 = lane & 3;
+  for (; ok;) {
+    const Segment sg = segment_of(x, start, end, c);
+    for (int i = sg.lo; i < sg.hi; ++i, ++t) {
+      const uint32_t stage = kv * H + t % H;
+      // every tile's free slot is waited for here, in order (a barrier's parity tells only one
+      // use from the next); a block tile's is handed on to its producer warp, by both converter
+      // warps and on a barrier of that slot, so that no barrier runs ahead of one who waits on it
+      ok = mbar_wait_warp(smem_u32(&bars->kv_empty[stage]), ((t / H) & 1) ^ 1, wc);
+      if (!ok) break;
+      if (i < p.blk_tiles) {
+        if (lane == 0) mbar_arrive(smem_u32(&bars->blk_go[stage]));
+        continue;
+      }
+      const uint32_t piece = k % C::kRaw;
+      ok = mbar_wait_warp(smem_u32(&bars->raw_full[w][piece]), (k / C::kRaw) & 1, wc);
+      if (!ok) break;
+      const uint8_t* in = raw + piece * C::kRawBytes;
+      uint8_t* tile = smem + C::kStageOff + stage * C::kSlotBytes + first_row * kRowBytes;
+      const TileKeys tk = tile_keys(p, x, i);
+      const int n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
+      const uint32_t mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask);
+      const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
+#pragma unroll
+      for (int r0 = 0; r0 < 32; r0 += 8) {
+        if (r0 >= n) break;
+        const int row = r0 + (lane >> 2);
+        const bool seen = (mask >> row) & 1u;
+#pragma unroll
+        for (int e = 0; e < C::kHalves; ++e) {
+          const int hf = C::kHalves == 2 ? e ^ (row & 1) : 0;
+          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+          if (seen) {
+            const uint4 b = *reinterpret_cast<const uint4*>(in + row * D + hf * 64 + k4 * 16);
+            const uint32_t byte = in[C::kRawScale + (row + odd) * kRowScale + hf * 2 + (k4 >> 1)];
+            lo = mx_to_bf16x8(make_uint2(b.x, b.y), byte);
+            hi = mx_to_bf16x8(make_uint2(b.z, b.w), byte);
+          }
+          uint8_t* to = tile + hf * (NK * kRowBytes) + row * kRowBytes;
+          *reinterpret_cast<uint4*>(to + (((2 * k4) ^ (row & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(to + (((2 * k4 + 1) ^ (row & 7)) << 4)) = hi;
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();   // every lane has read the piece and written its share of the tile
+      if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[stage]));
+      ++k;
+      if (!a.done) {
+        load(a, piece);
+        ++issued;
+        advance(a);
+      }
+    }
+    if (!ok || sg.last) break;
+    x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+  }
+  if (!ok) {
+    // copies that may still be landing in shared memory
+    int dummy = 0;
+    WaitCtx dw{&dummy, nullptr, 2000000ull};
+    for (; k < issued; ++k) mbar_wait(smem_u32(&bars->raw_full[w][k % C::kRaw]), (k / C::kRaw) & 1, dw);
+  }
+}
+
+template <int D, int NK, bool VIS, bool MX>
+__global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     attn_tcgen05_kernel(const Problem p, const __grid_constant__ TmaMaps maps) {
-  using C = Cfg<D, NK>;
-  constexpr int NBUF = C::kBufs;
+  using C = Cfg<D, NK, MX>;
+  constexpr int NBUF = C::kBufs, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t sbase = smem_u32(smem);
@@ -199,9 +372,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&bars->o_empty[m]), 128);
     }
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(smem_u32(&bars->kv_full[s]), 1);
+      mbar_init(smem_u32(&bars->kv_full[s]), MX ? 2 : 1);  // MX: the tile's two converter warps
       mbar_init(smem_u32(&bars->kv_empty[s]), MT);
     }
+    if (MX)
+      for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bars->blk_go[s]), 2);
+    for (int w = 0; w < 4; ++w)
+      for (int s = 0; s < C::kRaw; ++s)
+        mbar_init(smem_u32(&bars->raw_full[w][s]), 33);  // the expected bytes, 32 lanes' scale copies
     sh->abort_flag = 0;
     fence_barrier_init();
   }
@@ -241,6 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool have_work = start < end;
   if constexpr (C::kSplitRegs) {
     if (have_work && warp < 4) regs_dec<C::kCtrlRegs>();
+    if (have_work && warp >= 12) regs_dec<C::kConvRegs>();
   }
 
   if ((warp == 0 || warp == 3) && have_work) {
@@ -252,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // could behind V loads in one ring.
     constexpr int H = C::kStages / 2;
     const int kv = warp == 0 ? 0 : 1;
-    uint32_t t = 0, q_it = 0, tail_ph = 0;
+    uint32_t t = 0, q_it = 0, tail_ph = 0, go_ph = 0;
     bool ok = true;
     Unit x = sh->first;
     for (; ok;) {
@@ -280,16 +459,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = paged_row(p, x.n, x.h, tk.first + lane * psub);
         return row < 0 ? (p.num_pages * p.Hkv) << p.page_shift : row;  // a bad page reads as zeros
       };
-      int cur_row = slice_row(sg.lo);
-      for (int i = sg.lo; i < sg.hi && ok; ++i, ++t) {
+      int cur_row = MX ? 0 : slice_row(sg.lo);
+      const int hi = MX ? min(sg.hi, p.blk_tiles) : sg.hi;   // (MX: context tiles come from the converters)
+      for (int i = sg.lo; i < hi && ok; ++i, ++t) {
         const TileKeys tk = tile_keys(p, x, i);
         const int box_rows = tk.is_blk ? min(p.S, NK) : (p.page_table ? ceil_div(tk.count, psub) * psub : NK);
         const uint32_t bytes = (uint32_t)(box_rows * kRowBytes * C::kHalves);
         const int nsl = p.page_table && !tk.is_blk ? box_rows / psub : 0;   // slices of a paged tile
         const int row_i = cur_row;
-        if (i + 1 < sg.hi) cur_row = slice_row(i + 1);
+        if (!MX && i + 1 < sg.hi) cur_row = slice_row(i + 1);
         const int s = kv * H + (int)(t % H);
-        ok = mbar_wait(smem_u32(&bars->kv_empty[s]), ((t / H) & 1) ^ 1, wc);
+        if constexpr (MX) {
+          ok = mbar_wait(smem_u32(&bars->blk_go[s]), (go_ph >> s) & 1, wc);
+          go_ph ^= 1u << s;
+        } else ok = mbar_wait(smem_u32(&bars->kv_empty[s]), ((t / H) & 1) ^ 1, wc);
         if (!ok) break;
         const uint32_t slot = kv_s + s * C::kSlotBytes;
         const CUtensorMap* m = tk.is_blk ? (kv ? &maps.v_blk : &maps.k_blk) : (kv ? &maps.v_ctx : &maps.k_ctx);
@@ -326,6 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_2d(dst, m, bar, hf * 64, ctx_row0 + tk.first);
           }
         }
+        if (MX && lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));   // for the second converter warp
         if (fix) {
           ok = mbar_wait(smem_u32(&bars->tail), tail_ph, wc);
           tail_ph ^= 1;
@@ -346,6 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));
         }
       }
+      if (MX) t += sg.hi - max(sg.lo, hi);
       if (!ok || sg.last) break;
       x = make_unit(p, x.u + 1, x.Tu + x.tiles);
     }
@@ -463,6 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     WaitCtx dw{&dummy, nullptr, 2000000ull};
     mbar_wait(smem_u32(&bars->drain), 0, dw);
     __syncwarp();
+  } else if (MX && warp >= 12 && have_work) {
+    convert_tiles<D, NK>(p, sh, bars, smem, wc, c, warp - 12, lane);
   } else if (warp >= 4 && have_work) {
     // ========================================================= softmax WGs ==
     if constexpr (C::kSplitRegs) regs_inc<C::kSoftmaxRegs>();
@@ -636,23 +823,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (p.arrivals != nullptr)
-    fused_combine<D>(p, T, start, end, sh->first, *(volatile int*)&sh->abort_flag != 0);
+    fused_combine<D, kThreads, MX ? 8 : 16>(p, T, start, end, sh->first, *(volatile int*)&sh->abort_flag != 0);
 }
 
-template <int D, int NK, bool VIS = false>
+template <int D, int NK, bool VIS = false, bool MX = false>
 void set_smem_attr() {
-  cudaFuncSetAttribute(attn_tcgen05_kernel<D, NK, VIS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       Cfg<D, NK>::kSmemBytes);
+  cudaFuncSetAttribute(attn_tcgen05_kernel<D, NK, VIS, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                       Cfg<D, NK, MX>::kSmemBytes);
 }
 
-template <int D, int NK, bool VIS = false>
+template <int D, int NK, bool VIS = false, bool MX = false>
 cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
   // a programmatic dependent of the previous kernel on the stream (its setup overlaps that
   // kernel's tail), and cooperative when the fused combine needs every CTA resident at once
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<D, NK>::kSmemBytes;
+  cfg.blockDim = dim3(Cfg<D, NK, MX>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Cfg<D, NK, MX>::kSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -661,7 +848,7 @@ cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
   attr[1].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.arrivals != nullptr ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK, VIS>, p, maps);
+  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK, VIS, MX>, p, maps);
 }
 
 }  // namespace
@@ -676,10 +863,16 @@ cudaError_t launch_attn_tcgen05(const Problem& p, const TmaMaps& maps, cudaStrea
     set_smem_attr<64, 64>();
     set_smem_attr<128, 64, true>();
     set_smem_attr<64, 64, true>();
+    set_smem_attr<128, 64, true, true>();
+    set_smem_attr<64, 64, true, true>();
     return true;
   }();
   (void)attr_done;
   if (!tcgen05_key_tile_supported(p.key_tile)) return cudaErrorInvalidValue;
+  if (p.k_scale) {   // quantised context
+    if (p.key_tile != 64) return cudaErrorInvalidValue;
+    return p.D == 128 ? launch<128, 64, true, true>(p, maps, stream) : launch<64, 64, true, true>(p, maps, stream);
+  }
   // trees, and paged windows whose first load may start before the window: 64-key tiles
   if (p.parents || (p.window > 0 && p.win_align > 1)) {
     if (p.key_tile != 64) return cudaErrorInvalidValue;

@@ -13,32 +13,38 @@ namespace tt {
 
 constexpr int kMxBlock = 32;   // elements per scale
 
-// Multipliers (each a bf16 pair of equal values) whose product is 2^(120 + e), e = byte - 127:
-// two factors, because 2^(120 + e) itself is beyond bf16 for e > 7.
-struct MxScale {
-  uint32_t a, b;
-};
-__device__ __forceinline__ MxScale mx_scale(uint32_t byte) {
-  const int e = (int)byte - 127;
-  const int h = e >> 1;
-  MxScale s;
-  s.a = (uint32_t)(60 + 127 + h) * 0x00800080u;        // exponent field at bit 7 of both halves
-  s.b = (uint32_t)(60 + 127 + e - h) * 0x00800080u;
-  return s;
+// A scale byte as multipliers of values that read 2^120 too small (mx_to_bf16x4): 2^(120 + e) as a
+// bf16 pair of equal values, and for e > 7, where that leaves bf16, the rest as a second one.
+constexpr uint32_t kMxOneFactor = 134;   // largest byte (e = 7) that one factor holds
+__device__ __forceinline__ uint32_t mx_factor(uint32_t byte) { return min(byte + 120u, 254u) * 0x00800080u; }
+__device__ __forceinline__ uint32_t mx_rest(uint32_t byte) {
+  return (127u + (byte > kMxOneFactor ? byte - kMxOneFactor : 0u)) * 0x00800080u;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t x, uint32_t y) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
   return r;
 }
-// Four e4m3 bytes -> four bf16 (two pairs, memory order), scaled.  The seven magnitude bits of a
-// byte moved under bf16's exponent field read as the value times 2^-120 (exact for e4m3's
-// subnormals too: they land on bf16 subnormals).
-__device__ __forceinline__ uint2 mx_to_bf16x4(uint32_t w, MxScale s) {
-  const uint32_t lo = __byte_perm(w, 0u, 0x1404), hi = __byte_perm(w, 0u, 0x3424);
-  const uint32_t x = (lo & 0x80008000u) | ((lo >> 4) & 0x07F007F0u);
-  const uint32_t y = (hi & 0x80008000u) | ((hi >> 4) & 0x07F007F0u);
-  return make_uint2(mul_bf16x2(mul_bf16x2(x, s.a), s.b), mul_bf16x2(mul_bf16x2(y, s.a), s.b));
+// Four e4m3 bytes -> four bf16 (two pairs, memory order) times `factor`.  Each byte is widened to 16
+// bits with its sign (the permute's sign mode) and moved up by four: its seven magnitude bits then lie
+// at the bottom of bf16's exponent and the top of its mantissa, which reads as the value times 2^-120
+// (exact for e4m3's subnormals too: they land on bf16 subnormals).
+__device__ __forceinline__ uint2 mx_to_bf16x4(uint32_t w, uint32_t factor) {
+  uint32_t x, y;
+  asm("prmt.b32 %0, %1, 0, 0x9180;" : "=r"(x) : "r"(w));
+  asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(y) : "r"(w));
+  return make_uint2(mul_bf16x2((x << 4) & 0x87F087F0u, factor), mul_bf16x2((y << 4) & 0x87F087F0u, factor));
+}
+// Eight bytes of one scale block -> eight bf16.
+__device__ __forceinline__ uint4 mx_to_bf16x8(uint2 w, uint32_t byte) {
+  const uint32_t f = mx_factor(byte);
+  const uint2 a = mx_to_bf16x4(w.x, f), b = mx_to_bf16x4(w.y, f);
+  uint4 r = make_uint4(a.x, a.y, b.x, b.y);
+  if (byte > kMxOneFactor) {
+    const uint32_t g = mx_rest(byte);
+    r = make_uint4(mul_bf16x2(r.x, g), mul_bf16x2(r.y, g), mul_bf16x2(r.z, g), mul_bf16x2(r.w, g));
+  }
+  return r;
 }
 
 }  // namespace tt
