@@ -263,58 +263,82 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
   for (; issued < (uint32_t)C::kRaw && !a.done; ++issued, advance(a)) load(a, issued);
   bool ok = true;
   Unit x = sh->first;
+  // lane's chunks of a piece: the k4-th 16 bytes of one half of row_of(e)
+  constexpr int kChunks = 4 * C::kHalves;
   const int k4 = lane & 3;
+  auto row_of = [&](int e) { return e / C::kHalves * 8 + (lane >> 2); };
+  auto half_of = [&](int e) { return C::kHalves == 2 ? (e ^ (lane >> 2)) & 1 : 0; };
   for (; ok;) {
     const Segment sg = segment_of(x, start, end, c);
     for (int i = sg.lo; i < sg.hi; ++i, ++t) {
       const uint32_t stage = kv * H + t % H;
+      const bool blk = i < p.blk_tiles;
+      // the piece's bytes into registers (16 of every 8th row's half, twice where a row has two), its
+      // slot on to the next piece
+      uint4 b[kChunks];
+      uint32_t byte[kChunks];
+      uint32_t mask = 0;
+      int n = 0;
+      if (!blk) {
+        const uint32_t piece = k % C::kRaw;
+        ok = mbar_wait_warp(smem_u32(&bars->raw_full[w][piece]), (k / C::kRaw) & 1, wc);
+        if (!ok) break;
+        const uint8_t* in = raw + piece * C::kRawBytes;
+        const TileKeys tk = tile_keys(p, x, i);
+        n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
+        const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
+        mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask);
+#pragma unroll
+        for (int e = 0; e < kChunks; ++e) {
+          const int row = row_of(e), hf = half_of(e);
+          b[e] = *reinterpret_cast<const uint4*>(in + row * D + hf * 64 + k4 * 16);
+          byte[e] = in[C::kRawScale + (row + odd) * kRowScale + hf * 2 + (k4 >> 1)];
+        }
+        __syncwarp();
+        ++k;
+        if (!a.done) {
+          load(a, piece);
+          ++issued;
+          advance(a);
+        }
+      }
       // every tile's free slot is waited for here, in order (a barrier's parity tells only one
       // use from the next); a block tile's is handed on to its producer warp, by both converter
       // warps and on a barrier of that slot, so that no barrier runs ahead of one who waits on it
       ok = mbar_wait_warp(smem_u32(&bars->kv_empty[stage]), ((t / H) & 1) ^ 1, wc);
       if (!ok) break;
-      if (i < p.blk_tiles) {
+      if (blk) {
         if (lane == 0) mbar_arrive(smem_u32(&bars->blk_go[stage]));
         continue;
       }
-      const uint32_t piece = k % C::kRaw;
-      ok = mbar_wait_warp(smem_u32(&bars->raw_full[w][piece]), (k / C::kRaw) & 1, wc);
-      if (!ok) break;
-      const uint8_t* in = raw + piece * C::kRawBytes;
       uint8_t* tile = smem + C::kStageOff + stage * C::kSlotBytes + first_row * kRowBytes;
-      const TileKeys tk = tile_keys(p, x, i);
-      const int n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
-      const uint32_t mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask);
-      const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
+      auto store = [&](int e, uint4 lo, uint4 hi) {
+        uint8_t* to = tile + half_of(e) * (NK * kRowBytes) + row_of(e) * kRowBytes;
+        *reinterpret_cast<uint4*>(to + (((2 * k4) ^ (row_of(e) & 7)) << 4)) = lo;
+        *reinterpret_cast<uint4*>(to + (((2 * k4 + 1) ^ (row_of(e) & 7)) << 4)) = hi;
+      };
+      uint32_t top = 0;
 #pragma unroll
-      for (int r0 = 0; r0 < 32; r0 += 8) {
-        if (r0 >= n) break;
-        const int row = r0 + (lane >> 2);
-        const bool seen = (mask >> row) & 1u;
+      for (int e = 0; e < kChunks; ++e) top = max(top, byte[e]);
+      if (__all_sync(0xffffffffu, mask == 0xffffffffu && top <= kMxOneFactor)) {
 #pragma unroll
-        for (int e = 0; e < C::kHalves; ++e) {
-          const int hf = C::kHalves == 2 ? e ^ (row & 1) : 0;
-          uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-          if (seen) {
-            const uint4 b = *reinterpret_cast<const uint4*>(in + row * D + hf * 64 + k4 * 16);
-            const uint32_t byte = in[C::kRawScale + (row + odd) * kRowScale + hf * 2 + (k4 >> 1)];
-            lo = mx_to_bf16x8(make_uint2(b.x, b.y), byte);
-            hi = mx_to_bf16x8(make_uint2(b.z, b.w), byte);
-          }
-          uint8_t* to = tile + hf * (NK * kRowBytes) + row * kRowBytes;
-          *reinterpret_cast<uint4*>(to + (((2 * k4) ^ (row & 7)) << 4)) = lo;
-          *reinterpret_cast<uint4*>(to + (((2 * k4 + 1) ^ (row & 7)) << 4)) = hi;
+        for (int e = 0; e < kChunks; ++e) {
+          const uint32_t f = mx_factor(byte[e]);
+          const uint2 b0 = mx_to_bf16x4(b[e].x, f), b1 = mx_to_bf16x4(b[e].y, f);
+          const uint2 b2 = mx_to_bf16x4(b[e].z, f), b3 = mx_to_bf16x4(b[e].w, f);
+          store(e, make_uint4(b0.x, b0.y, b1.x, b1.y), make_uint4(b2.x, b2.y, b3.x, b3.y));
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < kChunks; ++e) {
+          if (row_of(e) >= n) continue;
+          if (!((mask >> row_of(e)) & 1u)) b[e] = make_uint4(0, 0, 0, 0);
+          store(e, mx_to_bf16x8(make_uint2(b[e].x, b[e].y), byte[e]), mx_to_bf16x8(make_uint2(b[e].z, b[e].w), byte[e]));
         }
       }
       fence_proxy_async_smem();
-      __syncwarp();   // every lane has read the piece and written its share of the tile
+      __syncwarp();   // every lane has written its share of the tile
       if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[stage]));
-      ++k;
-      if (!a.done) {
-        load(a, piece);
-        ++issued;
-        advance(a);
-      }
     }
     if (!ok || sg.last) break;
     x = make_unit(p, x.u + 1, x.Tu + x.tiles);
