@@ -77,6 +77,8 @@ def lib() -> ctypes.CDLL:
     L.tt_block_attn.argtypes = [vp] * 10
     L.tt_block_attn_block_causal.argtypes = [vp] * 9
     L.tt_block_attn_paged.argtypes = [vp, vp, vp, vp, vp, i, i, i, vp, vp, vp, vp, vp, vp]
+    L.tt_block_attn_block_causal_backward.argtypes = [vp] * 13
+    L.tt_kv_append.argtypes = [vp] * 6 + [i, vp]
     L.tt_block_attn_host.argtypes = [vp] * 10
     L.tt_block_attn_check.argtypes = [vp, vp]
     L.tt_block_attn_profile.argtypes = [vp, i]
@@ -131,7 +133,7 @@ def _ptr(t):
 def _arg(t, name, numel, kind, device):
     """Check one tensor argument before its address reaches the library, whose kernels
     trust every size: ``kind`` "bf16" (any 2-byte type: bf16 values or their bit
-    patterns), "f32", "i32", "w32" (any 4-byte integer) or "u8" (any 1-byte type); ``numel`` the element count the
+    patterns), "f32", "i32", "w32" (any 4-byte integer), "u8" or "e4m3" (any 1-byte type); ``numel`` the element count the
     layout needs; ``device`` a CUDA ordinal, "host", or None (not checked).  None and raw integer addresses
     are passed through (the library rejects a null pointer it needs)."""
     if not isinstance(t, torch.Tensor):
@@ -139,7 +141,7 @@ def _arg(t, name, numel, kind, device):
     ok = {"bf16": t.element_size() == 2 and not t.is_floating_point() or t.dtype == torch.bfloat16,
           "f32": t.dtype == torch.float32, "i32": t.dtype == torch.int32,
           "w32": t.element_size() == 4 and not t.is_floating_point(),
-          "u8": t.element_size() == 1}[kind]
+          "u8": t.element_size() == 1, "e4m3": t.element_size() == 1}[kind]
     if not ok:
         raise TypeError(f"{name}: dtype {t.dtype} where {kind} is expected")
     if t.numel() != numel:
@@ -160,7 +162,34 @@ def _args(device, *items):
         _arg(t, name, numel, kind, device)
 
 
+# The type each kind of argument usually has; _addrs takes these without a further look.
+_USUAL = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
+          "e4m3": torch.float8_e4m3fn}
+
+
+def _addrs(device, items):
+    """Addresses of (tensor, name, numel, kind) items after the checks of _args.  A call's host time is
+    what a small decode waits for, so tensors of the usual type that pass are looked at once, with
+    the fewest calls into torch; whatever does not goes through _args, which says what is wrong."""
+    found = []
+    for t, _, numel, kind in items:
+        if t is None:
+            found.append(None)
+        elif (t.__class__ is torch.Tensor and t.dtype is _USUAL[kind] and t.numel() == numel
+              and t.get_device() == device and t.is_contiguous()):
+            found.append(t.data_ptr())
+        else:
+            break
+    else:
+        return found
+    _args(device, *items)
+    return [_ptr(t) for t, _, _, _ in items]
+
+
 def _stream(stream):
+    """A torch stream, a raw handle, or a Plan: the current stream of its device."""
+    if isinstance(stream, Plan):
+        return torch._C._cuda_getCurrentRawStream(stream.device)
     if stream is None:
         stream = torch.cuda.current_stream()
     if isinstance(stream, torch.cuda.Stream):
@@ -190,7 +219,7 @@ class MxCache:
         self.k, self.k_scale, self.v, self.v_scale, self.page_table = k, k_scale, v, v_scale, page_table
         self.shape = tuple(k.shape)
         n = k.numel()
-        items = [(k, "k", n, "u8"), (v, "v", n, "u8"), (k_scale, "k_scale", n // 32, "u8"),
+        items = [(k, "k", n, "e4m3"), (v, "v", n, "e4m3"), (k_scale, "k_scale", n // 32, "u8"),
                  (v_scale, "v_scale", n // 32, "u8")]
         num_pages = page_size = pages_per_seq = 0
         if page_table is not None:
@@ -199,9 +228,10 @@ class MxCache:
             num_pages, page_size, pages_per_seq = k.shape[0], k.shape[2], page_table.shape[1]
             items.append((page_table, "page_table", page_table.numel(), "i32"))
         self.device = k.device
-        _args(k.device.index if k.is_cuda else None, *items)
-        self._d = MxCacheDesc(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), num_pages, page_size,
-                              pages_per_seq)
+        # (a device cache's tensors are all on that device; a host one is refused by the calls)
+        at = _addrs(k.get_device() if k.is_cuda else None, items)
+        self._d = MxCacheDesc(at[0], at[1], at[2], at[3], at[4] if page_table is not None else None, num_pages,
+                              page_size, pages_per_seq)
         self._ref = ctypes.byref(self._d)
 
     @classmethod
@@ -266,35 +296,28 @@ class Plan:
         return inf
 
     # --- decode ------------------------------------------------------------
-    def block_attn(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out=None, lse=None, stream=None,
-                   want_lse=False):
+    # Each call lists its tensors in the C function's order of checks, and hands the addresses on.
+    def _outputs(self, q, out, lse, want_lse, tokens):
+        """out and lse as given, or new ones ([B, tokens, Hq, D], and [B, Hq, tokens] where wanted)."""
         s = self.shape
         if out is None:
-            out = torch.empty((s.batch, s.block, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
+            out = torch.empty((s.batch, tokens, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
         if lse is None and want_lse:
-            lse = torch.empty((s.batch, s.q_heads, s.block), dtype=torch.float32, device=q.device)
-        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
-              (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16"))
-        _check(lib().tt_block_attn(self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk),
-                                   _ptr(ctx_lens), _ptr(out), _ptr(lse), _stream(stream)), "tt_block_attn")
-        return (out, lse) if want_lse or lse is not None else out
+            lse = torch.empty((s.batch, s.q_heads, tokens), dtype=torch.float32, device=q.device)
+        return out, lse
 
     def _decode_items(self, q, k_blk, v_blk, ctx_lens, out, lse):
         s = self.shape
-        nq = s.batch * s.block * s.q_heads * s.head_dim
-        nb = s.batch * s.block * s.kv_heads * s.head_dim
-        return [(q, "q", nq, "bf16"), (k_blk, "k_blk", nb, "bf16"), (v_blk, "v_blk", nb, "bf16"),
+        rows = s.batch * s.block
+        nq, nb = rows * s.q_heads * s.head_dim, rows * s.kv_heads * s.head_dim
+        return ((q, "q", nq, "bf16"), (k_blk, "k_blk", nb, "bf16"), (v_blk, "v_blk", nb, "bf16"),
                 (ctx_lens, "ctx_lens", s.batch, "i32"), (out, "out", nq, self._out_kind()),
-                (lse, "lse", s.batch * s.q_heads * s.block, "f32")]
+                (lse, "lse", rows * s.q_heads, "f32"))
 
-    def _decode_outputs(self, q, out, lse, want_lse):
+    def _slab_items(self, k_ctx, v_ctx):
         s = self.shape
-        if out is None:
-            out = torch.empty((s.batch, s.block, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((s.batch, s.q_heads, s.block), dtype=torch.float32, device=q.device)
-        return out, lse
+        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
+        return (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16")
 
     def _page_items(self, k_pages, v_pages, page_table):
         """(num_pages, page_size, pages_per_seq, items to check) of a paged context."""
@@ -312,71 +335,74 @@ class Plan:
             if page_table.dim() != 2 or page_table.shape[0] != s.batch:
                 raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [{s.batch}, pages_per_seq]")
             pages_per_seq = page_table.shape[1]
-        return int(num_pages), int(page_size), int(pages_per_seq), [
+        return int(num_pages), int(page_size), int(pages_per_seq), (
             (k_pages, "k_pages", pool_numel, "bf16"), (v_pages, "v_pages", pool_numel, "bf16"),
-            (page_table, "page_table", s.batch * pages_per_seq, "i32")]
+            (page_table, "page_table", s.batch * pages_per_seq, "i32"))
+
+    def _parents_item(self, parents):
+        return (parents, "parents", self.shape.batch * self.shape.block, "i32")
 
     def _out_kind(self):
         return "bf16" if self.out_dtype == torch.bfloat16 else "f32"
+
+    def _on(self, stream):
+        return _stream(self if stream is None else stream)
+
+    def block_attn(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out=None, lse=None, stream=None,
+                   want_lse=False):
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
+        q_, kb, vb, lens, o, l, kc, vc = _addrs(self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse)
+                                                + self._slab_items(k_ctx, v_ctx))
+        _check(lib().tt_block_attn(self._h, q_, kc, vc, kb, vb, lens, o, l, self._on(stream)), "tt_block_attn")
+        return (out, lse) if lse is not None else out
 
     def block_attn_paged(self, q, k_pages, v_pages, page_table, k_blk, v_blk, ctx_lens, out=None, lse=None,
                          stream=None, want_lse=False):
         """Decode over a paged context cache: k_pages / v_pages [num_pages, Hkv, P, D] bf16
         pools, page_table [B, pages_per_seq] int32 (device); P = k_pages.shape[2].  With no
         context at all, the pools and the table may be None."""
-        s = self.shape
-        if out is None:
-            out = torch.empty((s.batch, s.block, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((s.batch, s.q_heads, s.block), dtype=torch.float32, device=q.device)
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
         num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse), *items)
-        _check(lib().tt_block_attn_paged(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                                         int(num_pages), int(page_size), int(pages_per_seq), _ptr(k_blk),
-                                         _ptr(v_blk), _ptr(ctx_lens), _ptr(out), _ptr(lse), _stream(stream)),
-               "tt_block_attn_paged")
-        return (out, lse) if want_lse or lse is not None else out
+        q_, kb, vb, lens, o, l, kp, vp, tab = _addrs(
+            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + items)
+        _check(lib().tt_block_attn_paged(self._h, q_, kp, vp, tab, num_pages, page_size, pages_per_seq, kb, vb, lens,
+                                         o, l, self._on(stream)), "tt_block_attn_paged")
+        return (out, lse) if lse is not None else out
 
     def block_attn_tree(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, parents, out=None, lse=None, stream=None,
                         want_lse=False):
         """Decode whose block is a tree of drafted tokens: parents [B, S] int32 (-1: hangs on the last
         committed token, -2: absent).  Otherwise as block_attn."""
-        s = self.shape
-        out, lse = self._decode_outputs(q, out, lse, want_lse)
-        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
-              (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16"),
-              (parents, "parents", s.batch * s.block, "i32"))
-        _check(lib().tt_block_attn_tree(self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk),
-                                        _ptr(ctx_lens), _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)),
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
+        q_, kb, vb, lens, o, l, kc, vc, par = _addrs(
+            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + self._slab_items(k_ctx, v_ctx)
+            + (self._parents_item(parents),))
+        _check(lib().tt_block_attn_tree(self._h, q_, kc, vc, kb, vb, lens, par, o, l, self._on(stream)),
                "tt_block_attn_tree")
-        return (out, lse) if want_lse or lse is not None else out
+        return (out, lse) if lse is not None else out
 
     def block_attn_tree_paged(self, q, k_pages, v_pages, page_table, k_blk, v_blk, ctx_lens, parents, out=None,
                               lse=None, stream=None, want_lse=False):
         """block_attn_tree over a paged context cache (pages as block_attn_paged)."""
-        s = self.shape
-        out, lse = self._decode_outputs(q, out, lse, want_lse)
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
         num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse), *items,
-              (parents, "parents", s.batch * s.block, "i32"))
-        _check(lib().tt_block_attn_tree_paged(self._h, _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                                              num_pages, page_size, pages_per_seq, _ptr(k_blk), _ptr(v_blk),
-                                              _ptr(ctx_lens), _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)),
-               "tt_block_attn_tree_paged")
-        return (out, lse) if want_lse or lse is not None else out
+        q_, kb, vb, lens, o, l, kp, vp, tab, par = _addrs(
+            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + items
+            + (self._parents_item(parents),))
+        _check(lib().tt_block_attn_tree_paged(self._h, q_, kp, vp, tab, num_pages, page_size, pages_per_seq, kb, vb,
+                                              lens, par, o, l, self._on(stream)), "tt_block_attn_tree_paged")
+        return (out, lse) if lse is not None else out
 
     # --- quantised context cache ---------------------------------------------
     def block_attn_mx(self, q, cache, k_blk, v_blk, ctx_lens, parents=None, out=None, lse=None, stream=None,
                       want_lse=False):
         """Decode over a quantised context cache (MxCache); with ``parents`` the block is a drafted tree."""
-        s = self.shape
-        out, lse = self._decode_outputs(q, out, lse, want_lse)
-        _args(self.device, *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
-              (parents, "parents", s.batch * s.block, "i32"))
-        _check(lib().tt_block_attn_mx(self._h, _ptr(q), cache._fits(self), _ptr(k_blk), _ptr(v_blk), _ptr(ctx_lens),
-                                      _ptr(parents), _ptr(out), _ptr(lse), _stream(stream)), "tt_block_attn_mx")
-        return (out, lse) if want_lse or lse is not None else out
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
+        q_, kb, vb, lens, o, l, par = _addrs(
+            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + (self._parents_item(parents),))
+        _check(lib().tt_block_attn_mx(self._h, q_, cache._fits(self), kb, vb, lens, par, o, l, self._on(stream)),
+               "tt_block_attn_mx")
+        return (out, lse) if lse is not None else out
 
     def kv_append_mx(self, k_new, v_new, cache, ctx_lens, counts=None, advance=True, stream=None):
         """Quantise k_new/v_new [B, rows, Hkv, D] into the cache at [L_n, L_n + counts[n]) (all rows
@@ -386,11 +412,11 @@ class Plan:
             raise ValueError(f"k_new: shape {tuple(k_new.shape)}, expected [{s.batch}, rows, {s.kv_heads}, "
                              f"{s.head_dim}]")
         n = k_new.numel()
-        _args(self.device, (k_new, "k_new", n, "bf16"), (v_new, "v_new", n, "bf16"),
-              (ctx_lens, "ctx_lens", s.batch, "i32"), (counts, "counts", s.batch, "i32"))
-        _check(lib().tt_kv_append_mx(self._h, _ptr(k_new), _ptr(v_new), k_new.shape[1], _ptr(counts),
-                                     cache._fits(self), _ptr(ctx_lens), int(bool(advance)), _stream(stream)),
-               "tt_kv_append_mx")
+        kn, vn, lens, cnt = _addrs(self.device, ((k_new, "k_new", n, "bf16"), (v_new, "v_new", n, "bf16"),
+                                                 (ctx_lens, "ctx_lens", s.batch, "i32"),
+                                                 (counts, "counts", s.batch, "i32")))
+        _check(lib().tt_kv_append_mx(self._h, kn, vn, k_new.shape[1], cnt, cache._fits(self), lens,
+                                     int(bool(advance)), self._on(stream)), "tt_kv_append_mx")
 
     def kv_read_mx(self, cache, ctx_lens, starts, k_out, v_out, stream=None):
         """Positions [starts[n], starts[n] + rows) below ctx_lens[n] back as bf16 into k_out/v_out
@@ -400,44 +426,38 @@ class Plan:
             raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [{s.batch}, {s.kv_heads}, rows, "
                              f"{s.head_dim}]")
         n = k_out.numel()
-        _args(self.device, (k_out, "k_out", n, "bf16"), (v_out, "v_out", n, "bf16"),
-              (ctx_lens, "ctx_lens", s.batch, "i32"), (starts, "starts", s.batch, "i32"))
-        _check(lib().tt_kv_read_mx(self._h, cache._fits(self), _ptr(ctx_lens), _ptr(starts), k_out.shape[2],
-                                   _ptr(k_out), _ptr(v_out), _stream(stream)), "tt_kv_read_mx")
+        ko, vo, lens, st = _addrs(self.device, ((k_out, "k_out", n, "bf16"), (v_out, "v_out", n, "bf16"),
+                                                (ctx_lens, "ctx_lens", s.batch, "i32"),
+                                                (starts, "starts", s.batch, "i32")))
+        _check(lib().tt_kv_read_mx(self._h, cache._fits(self), lens, st, k_out.shape[2], ko, vo, self._on(stream)),
+               "tt_kv_read_mx")
         return k_out, v_out
 
     def block_attn_host(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out, lse=None, stream=None):
         """Host (ideally pinned) CPU tensors in and out; copies happen inside the library."""
-        s = self.shape
-        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
-        _args("host", *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse),
-              (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16"))
+        _args("host", *self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse), *self._slab_items(k_ctx, v_ctx))
         _check(lib().tt_block_attn_host(self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk),
-                                        _ptr(ctx_lens), _ptr(out), _ptr(lse), _stream(stream)),
+                                        _ptr(ctx_lens), _ptr(out), _ptr(lse), self._on(stream)),
                "tt_block_attn_host")
         return out
 
     # --- block-causal ------------------------------------------------------
     def block_attn_block_causal(self, q, k_ctx, v_ctx, k_blk, v_blk, out=None, lse=None, stream=None,
                                 want_lse=False):
-        s = self.shape
-        if out is None:
-            out = torch.empty((s.batch, s.seq_len, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
-        if lse is None and want_lse:
-            lse = torch.empty((s.batch, s.q_heads, s.seq_len), dtype=torch.float32, device=q.device)
-        _args(self.device, *self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse, self._out_kind()))
-        _check(lib().tt_block_attn_block_causal(self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk),
-                                                _ptr(v_blk), _ptr(out), _ptr(lse), _stream(stream)),
+        out, lse = self._outputs(q, out, lse, want_lse, self.shape.seq_len)
+        q_, kc, vc, kb, vb, o, l = _addrs(self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse,
+                                                                          self._out_kind()))
+        _check(lib().tt_block_attn_block_causal(self._h, q_, kc, vc, kb, vb, o, l, self._on(stream)),
                "tt_block_attn_block_causal")
-        return (out, lse) if want_lse or lse is not None else out
+        return (out, lse) if lse is not None else out
 
     def _causal_items(self, q, k_ctx, v_ctx, k_blk, v_blk, out, lse, out_kind="f32"):
         s = self.shape
         nq = s.batch * s.seq_len * s.q_heads * s.head_dim
         nk = s.batch * s.seq_len * s.kv_heads * s.head_dim
-        return [(q, "q", nq, "bf16"), (k_ctx, "k_ctx", nk, "bf16"), (v_ctx, "v_ctx", nk, "bf16"),
+        return ((q, "q", nq, "bf16"), (k_ctx, "k_ctx", nk, "bf16"), (v_ctx, "v_ctx", nk, "bf16"),
                 (k_blk, "k_blk", nk, "bf16"), (v_blk, "v_blk", nk, "bf16"), (out, "out", nq, out_kind),
-                (lse, "lse", s.batch * s.q_heads * s.seq_len, "f32")]
+                (lse, "lse", s.batch * s.q_heads * s.seq_len, "f32"))
 
     def block_causal_backward(self, q, k_ctx, v_ctx, k_blk, v_blk, out, lse, dout, dq=None, dk_blk=None,
                               dv_blk=None, stream=None):
@@ -453,12 +473,12 @@ class Plan:
             dv_blk = torch.empty_like(dk_blk)
         nq = s.batch * s.seq_len * s.q_heads * s.head_dim
         nk = s.batch * s.seq_len * s.kv_heads * s.head_dim
-        _args(self.device, *self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse),
-              (dout, "dout", nq, "bf16"), (dq, "dq", nq, "f32"), (dk_blk, "dk_blk", nk, "f32"),
-              (dv_blk, "dv_blk", nk, "f32"))
-        _check(lib().tt_block_attn_block_causal_backward(
-            self._h, _ptr(q), _ptr(k_ctx), _ptr(v_ctx), _ptr(k_blk), _ptr(v_blk), _ptr(out), _ptr(lse), _ptr(dout),
-            _ptr(dq), _ptr(dk_blk), _ptr(dv_blk), _stream(stream)), "tt_block_attn_block_causal_backward")
+        q_, kc, vc, kb, vb, o, l, do, dq_, dk, dv = _addrs(
+            self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse)
+            + ((dout, "dout", nq, "bf16"), (dq, "dq", nq, "f32"), (dk_blk, "dk_blk", nk, "f32"),
+               (dv_blk, "dv_blk", nk, "f32")))
+        _check(lib().tt_block_attn_block_causal_backward(self._h, q_, kc, vc, kb, vb, o, l, do, dq_, dk, dv,
+                                                         self._on(stream)), "tt_block_attn_block_causal_backward")
         return dq, dk_blk, dv_blk
 
     # --- committed-block cache update ------------------------------------------
@@ -467,19 +487,18 @@ class Plan:
         place; advance ctx_lens (device int32) by S when `advance`."""
         s = self.shape
         nb = s.batch * s.block * s.kv_heads * s.head_dim
-        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
-        _args(self.device, (k_new, "k_new", nb, "bf16"), (v_new, "v_new", nb, "bf16"), (k_ctx, "k_ctx", nc, "bf16"),
-              (v_ctx, "v_ctx", nc, "bf16"), (ctx_lens, "ctx_lens", s.batch, "i32"))
-        _check(lib().tt_kv_append(self._h, _ptr(k_new), _ptr(v_new), _ptr(k_ctx), _ptr(v_ctx), _ptr(ctx_lens),
-                                  int(bool(advance)), _stream(stream)), "tt_kv_append")
+        kn, vn, kc, vc, lens = _addrs(self.device, ((k_new, "k_new", nb, "bf16"), (v_new, "v_new", nb, "bf16"))
+                                      + self._slab_items(k_ctx, v_ctx) + ((ctx_lens, "ctx_lens", s.batch, "i32"),))
+        _check(lib().tt_kv_append(self._h, kn, vn, kc, vc, lens, int(bool(advance)), self._on(stream)),
+               "tt_kv_append")
 
     # --- status / timing ---------------------------------------------------
     def check(self, stream=None):
         """Synchronise and read the device error word; raise TTError on a device-side error."""
-        _check(lib().tt_block_attn_check(self._h, _stream(stream)), "tt_block_attn_check")
+        _check(lib().tt_block_attn_check(self._h, self._on(stream)), "tt_block_attn_check")
 
     def check_status(self, stream=None) -> int:
-        return lib().tt_block_attn_check(self._h, _stream(stream))
+        return lib().tt_block_attn_check(self._h, self._on(stream))
 
     def profile(self, enable: bool):
         _check(lib().tt_block_attn_profile(self._h, int(enable)), "tt_block_attn_profile")
