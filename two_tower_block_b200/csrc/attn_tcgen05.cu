@@ -42,9 +42,9 @@
 // same code as without VIS.  V rows that no row may see are cleared in shared memory, since a
 // weight of 0 does not hide an infinity or NaN in them.
 //
-// MX: the context is e4m3 with a scale byte per 32 elements.  Four more warps (12..15) bring the
-// context tiles in as they are and write them, as bf16, into the same ring (convert_tiles); the
-// producer warps keep Q and the block's own tiles.
+// MX: the context is e4m3 with a scale byte per 32 elements.  Warp 3 brings its tiles in as they are
+// (load_raw_tiles), four more warps (12..15) write them as bf16 into the ring (convert_tiles), and
+// warp 0 keeps Q and both of the block's own tiles.
 //
 // Every wait is bounded (ptx.cuh: mbar_wait); on a timeout the CTA raises the
 // error word, drains what it issued, frees TMEM and returns.
@@ -78,13 +78,14 @@ struct Cfg {
   static constexpr int kEpiBytes = 8 * 32 * 32 * 4;  // 8 softmax warps x 32 rows x 32 fp32
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
   static constexpr int kBarBytes = 896;
-  // MX: each converter warp's ring of raw pieces, 32 rows of e4m3, their scale bytes and a row mask
+  // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
   static constexpr int kRawOff = kBarOff + kBarBytes;
-  static constexpr int kRawScale = 32 * D;             // byte offsets within a piece
-  static constexpr int kRawMask = kRawScale + 32 * (D / kMxBlock) + 12;
-  static constexpr int kRawBytes = 32 * D + (D == 128 ? 160 : 96);
+  static constexpr int kRawScale = 2 * NK * D;                      // byte offsets within a slot
+  static constexpr int kScaleBytes = NK * (D / kMxBlock) + 16;
+  static constexpr int kRawMask = kRawScale + 2 * kScaleBytes;
+  static constexpr int kRawBytes = kRawMask + 16;
   static constexpr int kRaw = MX ? (D == 128 ? 3 : 6) : 0;
-  static constexpr int kSmemBytes = kRawOff + 4 * kRaw * kRawBytes + 1024;  // + alignment slack
+  static constexpr int kSmemBytes = kRawOff + kRaw * kRawBytes + 1024;  // + alignment slack
   // Register split: the 128-key variant keeps a full 128-score row per softmax thread (launch: 168
   // per thread = 65536 / 384 rounded down to 8); with converter warps the launch gives 128 and
   // the softmax takes its 176 from the others.
@@ -102,7 +103,7 @@ struct Bars {
   uint64_t pv_done[2], o_full[2], o_empty[2];
   uint64_t kv_full[16], kv_empty[16];
   uint64_t blk_go[16];      // MX: this slot is free for a block tile
-  uint64_t raw_full[4][6];  // MX: [converter warp][piece]
+  uint64_t raw_full[6], raw_empty[6];  // MX: the ring of raw tiles
 };
 
 struct Shared {
@@ -171,144 +172,140 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
   }
 }
 
-// MX: the context tiles, brought in as e4m3 and converted to bf16 in the ring's K or V half.  Converter
-// warp w of 0..3 takes rows [32 (w & 1), 32 (w & 1) + 32) of every K (w < 2) or V tile of the CTA's
-// range, in the producers' order.  It loads its own pieces, so no other warp has to wait for them: the
-// rows by untiled bulk copies (rows of a cache or page lie one after another), the scale bytes by
-// four-byte asynchronous copies, both counted by the piece's barrier, kRaw pieces ahead.  Then 16
-// bytes at a time become 32 bytes of the swizzled tile; rows that are not visible (or whose page
-// lies outside the pool) become zeros, so P V meets no other row.  In each quarter of a
-// warp, four lanes work on one 64-element half of a row and four on the other half of the next
-// row, which keeps both the loads and the swizzled stores free of bank conflicts.
+// MX: the context tiles of the CTA's range, brought in as they are: K and V rows in e4m3 by untiled bulk
+// copies (the rows of a cache or of a page lie one after another), the scale bytes by four-byte
+// asynchronous copies, both counted by the slot's barrier.  One warp, which waits for nothing else, so
+// that it stays kRaw tiles ahead of the conversion across units.
+template <int D, int NK>
+__device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
+                                               const WaitCtx& wc, int c, int lane) {
+  using C = Cfg<D, NK, true>;
+  constexpr int kRowScale = D / kMxBlock;
+  const uint8_t* src[2] = {reinterpret_cast<const uint8_t*>(p.k_ctx), reinterpret_cast<const uint8_t*>(p.v_ctx)};
+  const uint8_t* scales[2] = {p.k_scale, p.v_scale};
+  const long long start = sh->start, end = sh->end;
+  const int psh = p.page_table ? min(p.page_shift, 6) : 6;   // rows that lie together: 1 << psh
+  uint32_t k = 0;
+  bool ok = true;
+  Unit x = sh->first;
+  for (; ok;) {
+    const Segment sg = segment_of(x, start, end, c);
+    for (int i = max(sg.lo, p.blk_tiles); i < sg.hi; ++i, ++k) {
+      const uint32_t slot = k % C::kRaw;
+      ok = mbar_wait_warp(smem_u32(&bars->raw_empty[slot]), ((k / C::kRaw) & 1) ^ 1, wc);
+      if (!ok) break;
+      uint8_t* dst = smem + C::kRawOff + slot * C::kRawBytes;
+      const uint32_t bar = smem_u32(&bars->raw_full[slot]);
+      const TileKeys tk = tile_keys(p, x, i);
+      const int mine = min(max(tk.count - (lane << psh), 0), 1 << psh);   // rows of lane's slice
+      int row = 0;
+      if (mine > 0) {
+        const int pos = tk.first + (lane << psh);
+        row = p.page_table ? paged_row(p, x.n, x.h, pos) : (x.n * p.Hkv + x.h) * p.ctx_stride + pos;
+      }
+      const bool there = mine > 0 && row >= 0;   // (a page outside the pool: its rows read as zeros)
+      const uint32_t rows = __reduce_add_sync(0xffffffffu, there ? mine : 0);
+      const unsigned long long bits = there ? span_mask(0, mine) << (lane << psh) : 0ull;
+      const uint32_t m0 = __reduce_or_sync(0xffffffffu, (uint32_t)bits);
+      const uint32_t m1 = __reduce_or_sync(0xffffffffu, (uint32_t)(bits >> 32));
+      if (lane == 0) {
+        *reinterpret_cast<unsigned long long*>(dst + C::kRawMask) =
+            (((unsigned long long)m1 << 32) | m0) & span_mask(tk.head, NK);
+        mbar_arrive_expect_tx(bar, 2 * rows * D);
+      }
+      __syncwarp();
+      if (there) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+          bulk_load(smem_u32(dst) + (kv * NK + (lane << psh)) * D, src[kv] + (size_t)row * D, mine * D, bar);
+      }
+      // scale bytes in words of four; of a contiguous head_dim 64 cache the first word may hold the
+      // row in front of the tile's first (the converters skip it), the last word may be half a one
+      const int odd = D == 64 ? __shfl_sync(0xffffffffu, row, 0) & 1 : 0;
+#pragma unroll
+      for (int e = 0; e < 64; e += 32) {
+        const int r = (e + lane) * 4 / kRowScale - odd;        // first row of the word
+        const int s = p.page_table ? min(max(r, 0) >> psh, 31) : 0;
+        const int row_s = __shfl_sync(0xffffffffu, row, s);
+        const bool ok_s = __shfl_sync(0xffffffffu, there, s);
+        if (r < tk.count && ok_s) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+            cp_async_4(smem_u32(dst) + C::kRawScale + kv * C::kScaleBytes + (e + lane) * 4,
+                       scales[kv] + ((size_t)(row_s - (s << psh)) + r) * kRowScale, min(4, (tk.count - r) * kRowScale));
+        }
+      }
+      cp_async_mbar_arrive(bar);
+    }
+    if (!ok || sg.last) break;
+    x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+  }
+  if (!ok) {
+    // copies that may still be landing in shared memory
+    int dummy = 0;
+    WaitCtx dw{&dummy, nullptr, 2000000ull};
+    for (uint32_t j = k > (uint32_t)C::kRaw ? k - C::kRaw : 0; j < k; ++j)
+      mbar_wait(smem_u32(&bars->raw_full[j % C::kRaw]), (j / C::kRaw) & 1, dw);
+  }
+}
+
+// MX: converter warp w of 0..3 turns rows [32 (w & 1), 32 (w & 1) + 32) of every K (w < 2) or V raw tile
+// into bf16 in the ring's swizzled slot.  16 bytes at a time become 32; rows that are not visible
+// become zeros, so P V meets no other row.  In each quarter of a warp, four lanes work on one
+// 64-element half of a row and four on the other half of the next row, which keeps both the
+// loads and the swizzled stores free of bank conflicts.
 template <int D, int NK>
 __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                               const WaitCtx& wc, int c, int w, int lane) {
   using C = Cfg<D, NK, true>;
   constexpr int H = C::kStages / 2, kRowScale = D / kMxBlock;
   const int kv = w >> 1, first_row = 32 * (w & 1);
-  const uint8_t* src = reinterpret_cast<const uint8_t*>(kv ? p.v_ctx : p.k_ctx);
-  const uint8_t* scales = kv ? p.v_scale : p.k_scale;
-  uint8_t* raw = smem + C::kRawOff + w * C::kRaw * C::kRawBytes;
   const long long start = sh->start, end = sh->end;
-
-  // the CTA's context tiles in order, ahead of the conversion
-  struct Cursor {
-    Unit x;
-    Segment sg;
-    int i;
-    bool done;
-  };
-  auto settle = [&](Cursor& q) {
-    for (;;) {
-      q.i = max(q.i, p.blk_tiles);
-      if (q.i < q.sg.hi) return;
-      if (q.sg.last) {
-        q.done = true;
-        return;
-      }
-      q.x = make_unit(p, q.x.u + 1, q.x.Tu + q.x.tiles);
-      q.sg = segment_of(q.x, start, end, c);
-      q.i = q.sg.lo;
-    }
-  };
-  auto advance = [&](Cursor& q) {
-    ++q.i;
-    settle(q);
-  };
-  auto load = [&](const Cursor& q, uint32_t piece) {
-    uint8_t* dst = raw + piece * C::kRawBytes;
-    const uint32_t bar = smem_u32(&bars->raw_full[w][piece]);
-    const TileKeys tk = tile_keys(p, q.x, q.i);
-    const int n = min(max(tk.count - first_row, 0), 32);     // rows of this piece
-    const int psub = p.page_table ? min(1 << p.page_shift, 32) : 32;   // rows that lie together
-    const int mine = min(max(n - lane * psub, 0), psub);     // of them, lane's slice
-    int row = 0;
-    if (mine > 0) {
-      const int pos = tk.first + first_row + lane * psub;
-      row = p.page_table ? paged_row(p, q.x.n, q.x.h, pos) : (q.x.n * p.Hkv + q.x.h) * p.ctx_stride + pos;
-    }
-    const bool there = mine > 0 && row >= 0;
-    const uint32_t rows = __reduce_add_sync(0xffffffffu, there ? mine : 0);
-    const uint32_t bits = __reduce_or_sync(0xffffffffu, there ? (0xffffffffu >> (32 - mine)) << (lane * psub) : 0u);
-    if (lane == 0) {
-      const int head = min(max(tk.head - first_row, 0), 32);
-      *reinterpret_cast<uint32_t*>(dst + C::kRawMask) = head < 32 ? bits & (0xffffffffu << head) : 0u;
-      mbar_arrive_expect_tx(bar, rows * D);
-    }
-    __syncwarp();
-    if (there) bulk_load(smem_u32(dst) + lane * psub * D, src + (size_t)row * D, mine * D, bar);
-    // scale bytes in words of four; of a contiguous head_dim 64 cache the first word may hold the
-    // row in front of the piece's first (the converter skips it), the last word may be half a one
-    const int odd = D == 64 ? __shfl_sync(0xffffffffu, row, 0) & 1 : 0;
-#pragma unroll
-    for (int e = 0; e < (D == 64 ? 17 : 32); e += 32) {
-      const int r = (e + lane) * 4 / kRowScale - odd;        // first row of the word
-      const int s = p.page_table ? max(r, 0) / psub : 0;
-      const int row_s = __shfl_sync(0xffffffffu, row, s & 31);
-      const bool ok_s = __shfl_sync(0xffffffffu, there, s & 31);
-      if (r < n && ok_s)
-        cp_async_4(smem_u32(dst) + C::kRawScale + (e + lane) * 4, scales + ((size_t)(row_s - s * psub) + r) * kRowScale,
-                   min(4, (n - r) * kRowScale));
-    }
-    cp_async_mbar_arrive(bar);
-  };
-
-  Cursor a;
-  a.x = sh->first;
-  a.sg = segment_of(a.x, start, end, c);
-  a.i = a.sg.lo;
-  a.done = false;
-  settle(a);
-  uint32_t issued = 0, k = 0, t = 0;   // pieces loaded, pieces converted, tiles of the CTA passed
-  for (; issued < (uint32_t)C::kRaw && !a.done; ++issued, advance(a)) load(a, issued);
-  bool ok = true;
-  Unit x = sh->first;
-  // lane's chunks of a piece: the k4-th 16 bytes of one half of row_of(e)
+  // lane's chunks of a tile: the k4-th 16 bytes of one half of row_of(e)
   constexpr int kChunks = 4 * C::kHalves;
   const int k4 = lane & 3;
   auto row_of = [&](int e) { return e / C::kHalves * 8 + (lane >> 2); };
   auto half_of = [&](int e) { return C::kHalves == 2 ? (e ^ (lane >> 2)) & 1 : 0; };
+  uint32_t k = 0, t = 0;   // raw tiles converted, tiles of the CTA passed
+  bool ok = true;
+  Unit x = sh->first;
   for (; ok;) {
     const Segment sg = segment_of(x, start, end, c);
     for (int i = sg.lo; i < sg.hi; ++i, ++t) {
       const uint32_t stage = kv * H + t % H;
       const bool blk = i < p.blk_tiles;
-      // the piece's bytes into registers (16 of every 8th row's half, twice where a row has two), its
-      // slot on to the next piece
       uint4 b[kChunks];
       uint32_t byte[kChunks];
       uint32_t mask = 0;
       int n = 0;
       if (!blk) {
-        const uint32_t piece = k % C::kRaw;
-        ok = mbar_wait_warp(smem_u32(&bars->raw_full[w][piece]), (k / C::kRaw) & 1, wc);
+        const uint32_t slot = k % C::kRaw;
+        ok = mbar_wait_warp(smem_u32(&bars->raw_full[slot]), (k / C::kRaw) & 1, wc);
         if (!ok) break;
-        const uint8_t* in = raw + piece * C::kRawBytes;
+        const uint8_t* in = smem + C::kRawOff + slot * C::kRawBytes;
         const TileKeys tk = tile_keys(p, x, i);
         n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
         const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
-        mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask);
+        mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask + first_row / 8);
+        const uint8_t* sc = in + C::kRawScale + kv * C::kScaleBytes + (first_row + odd) * kRowScale;
+        in += (kv * NK + first_row) * D;
 #pragma unroll
         for (int e = 0; e < kChunks; ++e) {
-          const int row = row_of(e), hf = half_of(e);
-          b[e] = *reinterpret_cast<const uint4*>(in + row * D + hf * 64 + k4 * 16);
-          byte[e] = in[C::kRawScale + (row + odd) * kRowScale + hf * 2 + (k4 >> 1)];
+          b[e] = *reinterpret_cast<const uint4*>(in + row_of(e) * D + half_of(e) * 64 + k4 * 16);
+          byte[e] = sc[row_of(e) * kRowScale + half_of(e) * 2 + (k4 >> 1)];
         }
         __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[slot]));
         ++k;
-        if (!a.done) {
-          load(a, piece);
-          ++issued;
-          advance(a);
-        }
       }
       // every tile's free slot is waited for here, in order (a barrier's parity tells only one
       // use from the next); a block tile's is handed on to its producer warp, by both converter
       // warps and on a barrier of that slot, so that no barrier runs ahead of one who waits on it
+      // (the first use of a slot needs no word)
       ok = mbar_wait_warp(smem_u32(&bars->kv_empty[stage]), ((t / H) & 1) ^ 1, wc);
       if (!ok) break;
       if (blk) {
-        if (lane == 0) mbar_arrive(smem_u32(&bars->blk_go[stage]));
+        if (lane == 0 && t >= (uint32_t)H) mbar_arrive(smem_u32(&bars->blk_go[stage]));
         continue;
       }
       uint8_t* tile = smem + C::kStageOff + stage * C::kSlotBytes + first_row * kRowBytes;
@@ -342,12 +339,6 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
     }
     if (!ok || sg.last) break;
     x = make_unit(p, x.u + 1, x.Tu + x.tiles);
-  }
-  if (!ok) {
-    // copies that may still be landing in shared memory
-    int dummy = 0;
-    WaitCtx dw{&dummy, nullptr, 2000000ull};
-    for (; k < issued; ++k) mbar_wait(smem_u32(&bars->raw_full[w][k % C::kRaw]), (k / C::kRaw) & 1, dw);
   }
 }
 
@@ -401,9 +392,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     }
     if (MX)
       for (int s = 0; s < C::kStages; ++s) mbar_init(smem_u32(&bars->blk_go[s]), 2);
-    for (int w = 0; w < 4; ++w)
-      for (int s = 0; s < C::kRaw; ++s)
-        mbar_init(smem_u32(&bars->raw_full[w][s]), 33);  // the expected bytes, 32 lanes' scale copies
+    for (int s = 0; s < C::kRaw; ++s) {
+      mbar_init(smem_u32(&bars->raw_full[s]), 33);  // the expected bytes, 32 lanes' scale copies
+      mbar_init(smem_u32(&bars->raw_empty[s]), 4);  // the converter warps
+    }
     sh->abort_flag = 0;
     fence_barrier_init();
   }
@@ -446,7 +438,9 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     if (have_work && warp >= 12) regs_dec<C::kConvRegs>();
   }
 
-  if ((warp == 0 || warp == 3) && have_work) {
+  if (MX && warp == 3 && have_work) {
+    if constexpr (MX) load_raw_tiles<D, NK>(p, sh, bars, smem, wc, c, lane);
+  } else if ((warp == 0 || warp == 3) && have_work) {
     // =========================================================== producers ==
     // Warp 0 loads Q of each segment and the K tiles, warp 3 the V tiles, each into its own
     // half of the ring: K(t) of the CTA's t-th tile in stage t % H, V(t) in stage H + t % H
@@ -485,7 +479,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       };
       int cur_row = MX ? 0 : slice_row(sg.lo);
       const int hi = MX ? min(sg.hi, p.blk_tiles) : sg.hi;   // (MX: context tiles come from the converters)
-      for (int i = sg.lo; i < hi && ok; ++i, ++t) {
+      auto load_tile = [&](int i, int kv) {
         const TileKeys tk = tile_keys(p, x, i);
         const int box_rows = tk.is_blk ? min(p.S, NK) : (p.page_table ? ceil_div(tk.count, psub) * psub : NK);
         const uint32_t bytes = (uint32_t)(box_rows * kRowBytes * C::kHalves);
@@ -494,10 +488,12 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         if (!MX && i + 1 < sg.hi) cur_row = slice_row(i + 1);
         const int s = kv * H + (int)(t % H);
         if constexpr (MX) {
-          ok = mbar_wait(smem_u32(&bars->blk_go[s]), (go_ph >> s) & 1, wc);
-          go_ph ^= 1u << s;
+          if (t >= (uint32_t)H) {
+            ok = mbar_wait(smem_u32(&bars->blk_go[s]), (go_ph >> s) & 1, wc);
+            go_ph ^= 1u << s;
+          }
         } else ok = mbar_wait(smem_u32(&bars->kv_empty[s]), ((t / H) & 1) ^ 1, wc);
-        if (!ok) break;
+        if (!ok) return;
         const uint32_t slot = kv_s + s * C::kSlotBytes;
         const CUtensorMap* m = tk.is_blk ? (kv ? &maps.v_blk : &maps.k_blk) : (kv ? &maps.v_ctx : &maps.k_ctx);
         // V rows [count, round16(count)) are read by the last PV k-step: zero them (with VIS also
@@ -537,7 +533,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         if (fix) {
           ok = mbar_wait(smem_u32(&bars->tail), tail_ph, wc);
           tail_ph ^= 1;
-          if (!ok) break;
+          if (!ok) return;
           const int r0 = VIS ? 0 : tk.count, r1 = round16(tk.count);
           const int n16 = (r1 - r0) * 8 * C::kHalves;  // 16-byte chunks to clear
           for (int e = lane; e < n16; e += 32) {
@@ -553,6 +549,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));
         }
+      };
+      for (int i = sg.lo; i < hi && ok; ++i, ++t) {
+        load_tile(i, kv);
+        if (MX && ok) load_tile(i, 1);   // (warp 0 brings in both of a block tile)
       }
       if (MX) t += sg.hi - max(sg.lo, hi);
       if (!ok || sg.last) break;
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       int dummy = 0;
       WaitCtx dw{&dummy, nullptr, 2000000ull};
       for (uint32_t j = (t > (uint32_t)H ? t - H : 0); j < t; ++j)
-        mbar_wait(smem_u32(&bars->kv_full[kv * H + j % H]), (j / H) & 1, dw);
+        for (int h = kv; h < (MX ? 2 : kv + 1); ++h) mbar_wait(smem_u32(&bars->kv_full[h * H + j % H]), (j / H) & 1, dw);
       if (q_it) mbar_wait(smem_u32(&bars->q_full), (q_it - 1) & 1, dw);
     }
   } else if ((warp == 1 || (warp == 2 && MT == 2)) && have_work) {
@@ -673,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     mbar_wait(smem_u32(&bars->drain), 0, dw);
     __syncwarp();
   } else if (MX && warp >= 12 && have_work) {
-    convert_tiles<D, NK>(p, sh, bars, smem, wc, c, warp - 12, lane);
+    if constexpr (MX) convert_tiles<D, NK>(p, sh, bars, smem, wc, c, warp - 12, lane);
   } else if (warp >= 4 && have_work) {
     // ========================================================= softmax WGs ==
     if constexpr (C::kSplitRegs) regs_inc<C::kSoftmaxRegs>();
