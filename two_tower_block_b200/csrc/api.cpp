@@ -180,6 +180,7 @@ tt::Problem base_problem(tt_plan_t plan) {
   p.window = plan->window;
   p.sinks = plan->sinks;
   p.win_align = 1;
+  p.unit_cost = 0;
   p.parents = nullptr;
   return p;
 }
@@ -303,6 +304,8 @@ std::vector<long long> weighted_causal_starts(const std::vector<int>& pref, long
   return tab;
 }
 
+constexpr int kDecodeUnitCost = 5;   // key tiles
+
 // The context of a decode call: contiguous slabs, or pages; bf16, or e4m3 with scales.
 struct CtxCache {
   const void *k, *v;
@@ -390,6 +393,8 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
   p.v_scale = c.v_scale;
   p.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
   p.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
+  // ragged batches: a unit costs about five tiles beyond its own (sched.cuh) on the default kernel
+  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 0) p.unit_cost = kDecodeUnitCost;
   p.ctx_lens = ctx_lens;
   p.parents = parents;
   p.out = out;

@@ -38,7 +38,7 @@
 // VIS: tiles in which a row sees only some keys beyond a valid prefix -- a drafted tree's block
 // tiles (each row sees itself and its ancestors) and the first tile of a paged window (the load
 // starts at a page slice, before the window).  The softmax then selects by a 64-bit mask per row,
-// built by walking the row's parents (at most S steps, once per block tile); full tiles run the
+// built by every warp for itself (walker.cuh: tree_rows) once per block tile; full tiles run the
 // same code as without VIS.  V rows that no row may see are cleared in shared memory, since a
 // weight of 0 does not hide an infinity or NaN in them.
 //
@@ -79,7 +79,8 @@ struct Cfg {
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
   static constexpr int kBarBytes = 896;
   // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
-  static constexpr int kRawOff = kBarOff + kBarBytes;
+  static constexpr int kTreeOff = kBarOff + kBarBytes;   // a tree's absent rows, for the V tiles
+  static constexpr int kRawOff = kTreeOff + kMaxRows * 2;
   static constexpr int kRawScale = 2 * NK * D;                      // byte offsets within a slot
   static constexpr int kScaleBytes = NK * (D / kMxBlock) + 16;
   static constexpr int kRawMask = kRawScale + 2 * kScaleBytes;
@@ -109,44 +110,38 @@ struct Bars {
 struct Shared {
   uint32_t tmem_base;
   int abort_flag;
+  unsigned arrival;       // the count that this launch's arrivals reach (fused combine)
   long long T, start, end;
-  Unit first;
+  Unit first, last;       // of the range
 };
 static_assert(sizeof(Bars) + sizeof(Shared) <= 896, "barrier block overflows its shared-memory slot");
 
 // Fused split combine (cooperative launch only: every CTA is resident).  Once its segments and
 // partials are written, each CTA adds one to its range's arrival count; every range does so
-// exactly once per launch, so all counts of a launch are equal.  For each cut unit with a
+// exactly once per launch, so all counts of a launch are equal, and one more than this range's before
+// it (`k`, read at the start).  For each cut unit with a
 // segment in this range (at most two: the unit holding the range's first tile and the one
-// holding its last), the CTA waits until every range of that unit has reached its own count,
+// holding its last), the CTA waits until every range of that unit has reached the count,
 // then combines its share of the unit's rows: rows [i R / n, (i + 1) R / n) for the i-th of the
 // unit's n ranges, one warp per row.  No CTA waits for ranges outside its units.  The waits
 // are bounded; a CTA that gave up (or whose pipeline aborted) combines nothing and the error
 // word says so.
-template <int D, int THREADS, int PARTS>   // PARTS: partials of a row in flight
+template <int D, int THREADS, int PARTS, int ROWS>   // partials of a row, and rows, in flight per warp
 __device__ __forceinline__ void fused_combine(const Problem& p, long long T, long long start, long long end,
-                                              const Unit& first, bool aborted) {
-  __shared__ unsigned s_k;
+                                              const Unit& first, const Unit& last, unsigned k, bool aborted) {
   __shared__ int s_ok;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
   __syncthreads();  // every write of this CTA precedes its arrival
-  if (tid == 0) {
-    __threadfence();
-    s_k = atomicAdd(p.arrivals + c, 1u) + 1u;
-  }
-  __syncthreads();
+  if (tid == 0) red_release_gpu_add(p.arrivals + c, 1u);
   if (start >= end || aborted) return;
-  const unsigned k = s_k;
   const int Ce = used_ranges(T, p.C);
-  Unit last = first;
-  while (last.Tu + last.tiles < end) last = make_unit(p, last.u + 1, last.Tu + last.tiles);
   for (int which = 0; which < 2; ++which) {
-    const Unit x = which == 0 ? first : last;
+    const Unit& x = which == 0 ? first : last;
     if (which == 1 && last.u == first.u) break;
-    if (x.Tu >= start && x.Tu + x.tiles <= end) continue;  // whole in this range: not cut
+    if (first_tile(x) >= start && end_tile(x) <= end) continue;  // whole in this range: not cut
     const long long* tab = range_table(p);
-    const int c0 = range_of_tile_tab(tab, T, Ce, x.Tu), c1 = range_of_tile_tab(tab, T, Ce, x.Tu + x.tiles - 1);
+    const int c0 = range_of_tile_tab(tab, T, Ce, first_tile(x)), c1 = range_of_tile_tab(tab, T, Ce, end_tile(x) - 1);
     if (warp == 0) {
       bool ok = true;
       const unsigned long long t0 = globaltimer_ns();
@@ -157,7 +152,6 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
             ok = false;
             break;
           }
-          __nanosleep(32);
         }
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -166,9 +160,10 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     __syncthreads();
     if (!s_ok) return;
     const int n = c1 - c0 + 1, i = c - c0;
-    const SplitRecord rec{x.u, c1, x.Tu == range_start_tab(tab, T, Ce, c0) ? 0 : 1, 0};
+    const SplitRecord rec{x.u, c1, first_after(x, range_start_tab(tab, T, Ce, c0)) ? 0 : 1, 0};
     const int r0 = (int)((long long)i * p.R / n), r1 = (int)((long long)(i + 1) * p.R / n);
-    for (int r = r0 + warp; r < r1; r += THREADS / 32) combine_row<D, PARTS>(p, c0, rec, r, lane);
+    constexpr int kWarps = THREADS / 32;
+    for (int r = r0 + warp; r < r1; r += ROWS * kWarps) combine_rows<D, PARTS, ROWS>(p, x, c0, rec, r, kWarps, r1, lane);
   }
 }
 
@@ -238,7 +233,7 @@ __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* s
       cp_async_mbar_arrive(bar);
     }
     if (!ok || sg.last) break;
-    x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+    x = next_unit(p, x);
   }
   if (!ok) {
     // copies that may still be landing in shared memory
@@ -338,7 +333,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[stage]));
     }
     if (!ok || sg.last) break;
-    x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+    x = next_unit(p, x);
   }
 }
 
@@ -423,6 +418,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       sh->start = start;
       sh->end = end;
       if (start < end) sh->first = first;
+      if (p.arrivals != nullptr) sh->arrival = __ldcg(p.arrivals + c) + 1u;
     }
   }
   tc_fence_before();
@@ -503,11 +499,13 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           if (kv == 1) {
             zero = span_mask(0, round16(tk.count)) & ~span_mask(tk.head, tk.count);
             if (tk.is_blk && p.parents) {
+              short* up = reinterpret_cast<short*>(smem + C::kTreeOff);
+              if (tk.first == 0) tree_rows(p, x.n, 0, lane, up, nullptr);
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
-                bool absent = false;
-                if (32 * w + lane < tk.count) tree_mask(p, x.n, tk.first + 32 * w + lane, tk.first, absent);
-                zero |= (unsigned long long)__ballot_sync(0xffffffffu, absent) << (32 * w);
+                const int t = 32 * w + lane;
+                zero |= (unsigned long long)__ballot_sync(0xffffffffu, t < tk.count && up[tk.first + t] == kAbsent)
+                        << (32 * w);
               }
             }
           }
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       }
       if (MX) t += sg.hi - max(sg.lo, hi);
       if (!ok || sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
     if (!ok) {
       // drain: wait (briefly) for loads that may still be landing in shared memory
@@ -663,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       __syncwarp();
       ++seg_cnt;
       if (sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
     // drain every MMA this warp issued before TMEM can be released
     if (elect_one()) tc_commit(smem_u32(&bars->drain));
@@ -686,6 +684,9 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       const uint32_t s_base = tmem + lane_off + m * 128;  // + buffer * NK
       const uint32_t o_addr = tmem + lane_off + 256 + m * D;
       float* stage = epi + (warp - 4) * 32 * 32;
+      unsigned long long* tree_sees = reinterpret_cast<unsigned long long*>(stage);      // [S <= 256]
+      short* tree_up = reinterpret_cast<short*>(tree_sees + kMaxRows);                     // [S]
+      const uint32_t gm = div_by(p.g);
       uint32_t G = 0, seg_cnt = 0;
       bool ok = true;
       Unit x = sh->first;
@@ -694,8 +695,12 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         float m_ref = -INFINITY, l = 0.f;
         // a row that a tree leaves out (or whose ancestors are left out) sees nothing
         bool absent = false;
+        const int tok = VIS ? row_token(min(r, p.R - 1), gm) : 0;
         if constexpr (VIS) {
-          if (p.parents) tree_mask(p, x.n, min(r, p.R - 1) / p.g, 0, absent);
+          if (p.parents) {   // (the warp's staging rows are free until the epilogue)
+            tree_rows(p, x.n, 0, lane, tree_up, tree_sees);
+            absent = tree_up[tok] == kAbsent;
+          }
         }
         // One tile of the softmax: its S row in registers, the row maximum in log2 units, the
         // lazy rescale of O, then P (bf16) over the S buffer.  Full tiles and the masked last
@@ -751,8 +756,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
             full = full && tk.head == 0 && !tree;
             if (!full) {
               mask = span_mask(tk.head, count);
-              bool a = false;
-              if (tree) mask &= tree_mask(p, x.n, min(r, p.R - 1) / p.g, tk.first, a);
+              if (tree) {
+                if (tk.first > 0) tree_rows(p, x.n, tk.first, lane, tree_up, tree_sees);
+                mask &= absent ? 0ull : tree_sees[tok];
+              }
             }
           }
           const int b = G % NBUF;
@@ -780,6 +787,16 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         const bool none = VIS && (absent || l == 0.f);   // no visible key: 0, lse = -inf
         const float inv = none ? 0.f : 1.f / l;
         const int rbase = m * 128 + q4 * 32;  // first packed row of this warp
+        // element offsets of the rows that this lane stores (every fourth) from the unit's first row in
+        // the output, or the segment's in the partials
+        const size_t at0 = (sg.full ? ((size_t)x.ns * p.S * p.Hq + x.h * p.g) * D : (size_t)sg.slot * p.R * D) + (lane & 7) * 4;
+        int at[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int gr = min(rbase + k * 4 + (lane >> 3), p.R - 1);
+          const int t = row_token(gr, gm);
+          at[k] = (sg.full ? t * p.Hq + (gr - t * p.g) : gr) * D;
+        }
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tmem_ld32(o_addr + cc * 32, o);
@@ -807,8 +824,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
             const int gr = rbase + rr;
             if (gr < p.R) {
               float4 f = reinterpret_cast<const float4*>(stage + rr * 32)[q ^ (rr & 7)];
-              if (sg.full) store_out4(p, out_offset(p, x, gr, D) + cc * 32 + q * 4, f);
-              else *reinterpret_cast<float4*>(out_row(p, x, sg, gr, D) + cc * 32 + q * 4) = f;
+              if (sg.full) store_out4(p, at0 + at[k] + cc * 32, f);
+              else *reinterpret_cast<float4*>(p.part_o + at0 + at[k] + cc * 32) = f;
             }
           }
           __syncwarp();
@@ -817,7 +834,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * 0.6931471805599453f;
           if (sg.full) {
             if (p.lse) {
-              const int t = r / p.g, j = r - (r / p.g) * p.g;
+              const int t = row_token(r, gm), j = r - t * p.g;
               p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse;
             }
           } else {
@@ -826,20 +843,21 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         }
         ++seg_cnt;
         if (sg.last) break;
-        x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+        x = next_unit(p, x);
       }
     }
   }
 
-  // record for the combine: the cut unit (if any) that begins in this range
+  // for the combine: the range's last unit, and the record of the cut unit (if any) that begins in it
   if (tid == 64) {
     SplitRecord rec{-1, -1, 0, 0};
     if (have_work) {
       Unit x = sh->first;
-      while (x.Tu + x.tiles < end) x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      while (!last_before(x, end)) x = next_unit(p, x);
+      sh->last = x;
       rec = record_of(x, T, p.C, start, end, range_table(p));
     }
-    p.records[c] = rec;
+    if (p.arrivals == nullptr) p.records[c] = rec;
   }
 
   tc_fence_before();
@@ -847,7 +865,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (p.arrivals != nullptr)
-    fused_combine<D, kThreads, MX ? 8 : 16>(p, T, start, end, sh->first, *(volatile int*)&sh->abort_flag != 0);
+    fused_combine<D, kThreads, C::kSplitRegs ? 8 : 12, C::kSplitRegs ? 1 : 2>(p, T, start, end, sh->first, sh->last, sh->arrival,
+                                               *(volatile int*)&sh->abort_flag != 0);
 }
 
 template <int D, int NK, bool VIS = false, bool MX = false>

@@ -274,7 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok || sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
     if (!ok) {
       int dummy = 0;
@@ -319,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++seg_cnt;
         }
         if (!ok || sg.last) break;
-        x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+        x = next_unit(p, x);
       }
     }
     __syncwarp();
@@ -415,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         G += n;
         ++seg_cnt;
         if (sg.last) break;
-        x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+        x = next_unit(p, x);
       }
     }
     __syncwarp();
@@ -564,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       G += n;
       ++seg_cnt;
       if (sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
   }
 
@@ -573,7 +573,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     SplitRecord rec{-1, -1, 0, 0};
     if (have_work) {
       Unit x = ms->first;
-      while (x.Tu + x.tiles < end) x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      while (!last_before(x, end)) x = next_unit(p, x);
       rec = record_of(x, T, p.C, start, end, range_table(p));
     }
     p.records[c] = rec;

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok || sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
     if (!ok) {
       // drain: wait (briefly) for loads that may still be landing in shared memory
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         G += n;
         ++seg_cnt;
         if (sg.last) break;
-        x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+        x = next_unit(p, x);
       }
       // drain every MMA this thread issued before TMEM can be released
       tc_commit(smem_u32(&bars->drain));
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++seg_cnt;
       if (sg.last) break;
-      x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      x = next_unit(p, x);
     }
   }
 
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     SplitRecord rec{-1, -1, 0, 0};
     if (have_work) {
       Unit x = ms->first;
-      while (x.Tu + x.tiles < end) x = make_unit(p, x.u + 1, x.Tu + x.tiles);
+      while (!last_before(x, end)) x = next_unit(p, x);
       rec = record_of(x, T, p.C, start, end, range_table(p));
     }
     p.records[c] = rec;

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = blockIdx.y * kRowsPerBlock + warp;
   if (r >= p.R) return;
-  combine_row<D>(p, c, rec, r, lane);
+  combine_rows<D, 8, 1>(p, make_unit(p, rec.unit, 0), c, rec, r, 1, r + 1, lane);
 }
 
 // One thread waits on a barrier that nothing arrives at; the bounded wait must

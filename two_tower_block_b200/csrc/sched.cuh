@@ -16,6 +16,12 @@
 // combine kernel.  Only a range's first and last segment can belong to a cut
 // unit, so 2*C slots always suffice.
 //
+// A unit may also carry a fixed cost of F tiles (the Q load and the pipeline's restart before it, the
+// output after it): the global sequence then has F / 2 empty places before each unit's tiles and the
+// rest after them, T counts them too, and a boundary that falls on empty places cuts no unit.  A
+// range costs its tiles and one F for each unit's edge inside it, which is what the even split of
+// that sequence evens out.  F is kept small enough that every range holds a tile (fixed_cost).
+//
 // A plan may instead give the boundaries as a table starts[0..C'] (starts[0] = 0,
 // starts[C'] = T, strictly increasing), which the block-causal calls of the default
 // kernel use to weigh each unit's fixed cost (built by the plan on the host); everything
@@ -31,7 +37,11 @@
 
 namespace tt {
 
-TT_HD long long range_start(long long T, int C, int c) { return (long long)c * T / C; }
+// (32-bit divisions where they hold: these sit on the path before a kernel's first load)
+TT_HD long long range_start(long long T, int C, int c) {
+  if (T < (1ll << 31) / C) return (uint32_t)c * (uint32_t)T / (uint32_t)C;
+  return (long long)c * T / C;
+}
 
 // Ranges actually used: min(C, T), so that every used range holds at least one
 // tile and the ranges touching a cut unit are consecutive and all non-empty.
@@ -40,7 +50,18 @@ TT_HD int used_ranges(long long T, int C) { return T < (long long)C ? (int)T : C
 // Index of the range whose [start, end) contains global tile x (0 <= x < T):
 // the largest c with floor(c*T/C) <= x, i.e. ceil((x+1)*C/T) - 1.
 TT_HD int range_of_tile(long long T, int C, long long x) {
+  if (T < (1ll << 30) / C) return (int)((((uint32_t)x + 1u) * (uint32_t)C + (uint32_t)T - 1u) / (uint32_t)T) - 1;
   return (int)(((x + 1) * (long long)C + T - 1) / T) - 1;
+}
+
+// The fixed cost per unit that leaves a tile to every range: at most `want`, for U units of T tiles in
+// all over C ranges (any range is at least floor((T + U F) / C) places long, and must be longer than
+// the F empty places between two units).
+TT_HD int fixed_cost(long long T, long long U, int C, int want) {
+  if (U >= C) return want;
+  if (T < C) return 0;
+  const long long most = (T - C) / (C - U);
+  return most < want ? (int)most : want;
 }
 
 // The same two for a boundary table (null: the uniform split).

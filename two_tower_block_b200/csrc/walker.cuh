@@ -13,7 +13,8 @@ struct Unit {
   int n, h, b;    // sequence, KV head, block index within the sequence
   int ns;         // block-sequence index n * NB + b (row block of q / k_blk / out)
   int sink_tiles, wstart, head;  // context runs of a windowed layer (sched.cuh: CtxSpan)
-  long long Tu;   // first global tile of the unit
+  int cost;       // its fixed cost (sched.cuh), cost / 2 places of it before the tiles
+  long long Tu;   // first global place of the unit
 };
 
 __device__ __forceinline__ int clamp_len(const Problem& p, int n, bool report) {
@@ -29,10 +30,11 @@ __device__ __forceinline__ int unit_tiles_k(const Problem& p, int L) {
   return p.blk_tiles + ctx_span(L, p.window, p.sinks, p.win_align, p.key_tile).tiles;
 }
 
-__device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu) {
+__device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu, int cost = 0) {
   Unit x;
   x.u = u;
   x.Tu = Tu;
+  x.cost = cost;
   if (p.mode == kDecode) {
     x.n = u / p.Hkv;
     x.h = u - x.n * p.Hkv;
@@ -54,10 +56,16 @@ __device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu)
   return x;
 }
 
-__device__ __forceinline__ long long warp_sum_ll(long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+__device__ __forceinline__ Unit next_unit(const Problem& p, const Unit& x) {
+  return make_unit(p, x.u + 1, x.Tu + x.tiles + x.cost, x.cost);
+}
+// Global places of the unit's first tile, and behind its last.
+__device__ __forceinline__ long long first_tile(const Unit& x) { return x.Tu + x.cost / 2; }
+__device__ __forceinline__ long long end_tile(const Unit& x) { return first_tile(x) + x.tiles; }
+// Whether no later unit has a tile before `end`, and no earlier one a tile at or after `start`.
+__device__ __forceinline__ bool last_before(const Unit& x, long long end) { return end_tile(x) + x.cost >= end; }
+__device__ __forceinline__ bool first_after(const Unit& x, long long start) {
+  return first_tile(x) - x.cost <= start;
 }
 
 // The boundary table of the call's split, or null for the uniform one.
@@ -65,20 +73,26 @@ __device__ __forceinline__ const long long* range_table(const Problem& p) {
   return p.mode == kDecode ? nullptr : p.causal_starts;
 }
 
-// Called by one full warp.  Finds the total tile count T, this range's
-// [start, end) and the unit containing `start` (valid only if start < end).
+// Called by one full warp.  Finds the total place count T, this range's
+// [start, end) and the first unit with a tile in it (valid only if start < end).
 __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T, long long& start,
                                            long long& end, Unit& first) {
   const int lane = threadIdx.x & 31;
+  int cost = 0, t = 0;   // t: tiles of a unit of sequence base + lane (total rows < 2^31: sums fit)
   if (p.mode == kDecode) {
-    long long tot = 0;
+    int tot = 0, least = INT32_MAX, most = 0;
     for (int base = 0; base < p.B; base += 32) {
-      int n = base + lane;
-      long long t = 0;
-      if (n < p.B) t = (long long)p.Hkv * unit_tiles_k(p, clamp_len(p, n, c == 0));
-      tot += warp_sum_ll(t);
+      const int n = base + lane;
+      t = n < p.B ? unit_tiles_k(p, clamp_len(p, n, c == 0)) : 0;
+      tot += __reduce_add_sync(0xffffffffu, t);
+      least = min(least, __reduce_min_sync(0xffffffffu, n < p.B ? t : INT32_MAX));
+      most = max(most, __reduce_max_sync(0xffffffffu, t));
     }
-    T = tot;
+    T = (long long)p.Hkv * tot;
+    // units of one length over ranges that divide them evenly need no weighing
+    const int U = p.B * p.Hkv;
+    if (p.unit_cost > 0 && !(least == most && p.C % U == 0)) cost = fixed_cost(T, U, p.C, p.unit_cost);
+    T += (long long)U * cost;
   } else {
     T = p.T_causal;
   }
@@ -93,24 +107,24 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
   if (p.mode == kDecode) {
     long long acc = 0;
     for (int base = 0; base < p.B; base += 32) {
-      int n = base + lane;
-      long long t = 0;
-      if (n < p.B) t = (long long)p.Hkv * unit_tiles_k(p, clamp_len(p, n, false));
-      long long incl = t;
+      const int n = base + lane;
+      if (p.B > 32) t = n < p.B ? unit_tiles_k(p, clamp_len(p, n, false)) : 0;
+      const int mine = n < p.B ? p.Hkv * (t + cost) : 0;
+      int incl = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
       }
-      long long total = __shfl_sync(0xffffffffu, incl, 31);
+      const int total = __shfl_sync(0xffffffffu, incl, 31);
       if (acc + total > start) {
-        unsigned m = __ballot_sync(0xffffffffu, acc + incl > start);
-        int src = __ffs(m) - 1;
-        long long pn = acc + __shfl_sync(0xffffffffu, incl - t, src);
-        int nn = base + src;
-        int tn = unit_tiles_k(p, clamp_len(p, nn, false));
-        int h = (int)((start - pn) / tn);
-        first = make_unit(p, nn * p.Hkv + h, pn + (long long)h * tn);
+        const int at = (int)(start - acc);
+        const int src = __ffs(__ballot_sync(0xffffffffu, incl > at)) - 1;
+        const int pn = __shfl_sync(0xffffffffu, incl - mine, src);
+        const int tn = __shfl_sync(0xffffffffu, t, src) + cost;
+        const int h = (at - pn) / tn;
+        first = make_unit(p, (base + src) * p.Hkv + h, acc + pn + h * tn, cost);
+        if (end_tile(first) <= start) first = next_unit(p, first);
         return;
       }
       acc += total;
@@ -138,13 +152,12 @@ struct Segment {
 
 __device__ __forceinline__ Segment segment_of(const Unit& x, long long start, long long end, int c) {
   Segment s;
-  long long lo = start > x.Tu ? start - x.Tu : 0;
-  long long hi = end - x.Tu < x.tiles ? end - x.Tu : x.tiles;
-  s.lo = (int)lo;
-  s.hi = (int)hi;
+  const long long f = first_tile(x);
+  s.lo = start > f ? (int)(start - f) : 0;
+  s.hi = end - f < x.tiles ? (int)(end - f) : x.tiles;
   s.full = (s.lo == 0 && s.hi == x.tiles);
-  s.slot = 2 * c + ((x.Tu + lo == start) ? 0 : 1);
-  s.last = (x.Tu + x.tiles >= end);
+  s.slot = 2 * c + (s.lo > 0 || first_after(x, start) ? 0 : 1);
+  s.last = last_before(x, end);
   return s;
 }
 
@@ -158,10 +171,10 @@ __device__ __forceinline__ SplitRecord record_of(const Unit& last, long long T, 
   r.last_range = -1;
   r.first_which = 0;
   r.pad = 0;
-  if (last.Tu >= start && last.Tu + last.tiles > end) {
+  if (first_tile(last) >= start && end_tile(last) > end) {
     r.unit = last.u;
-    r.last_range = range_of_tile_tab(tab, T, C, last.Tu + last.tiles - 1);
-    r.first_which = (last.Tu == start) ? 0 : 1;
+    r.last_range = range_of_tile_tab(tab, T, C, end_tile(last) - 1);
+    r.first_which = first_after(last, start) ? 0 : 1;
   }
   return r;
 }
@@ -171,6 +184,11 @@ __device__ __forceinline__ size_t out_offset(const Problem& p, const Unit& x, in
   const int t = r / p.g, j = r - (r / p.g) * p.g;
   return ((size_t)(x.ns * p.S + t) * p.Hq + x.h * p.g + j) * D;
 }
+// r / g for packed rows r < 256 of a unit (g <= 256): with m = ceil(2^16 / g) the product r m exceeds
+// r 2^16 / g by less than 2^8 <= 2^16 / g.
+__device__ __forceinline__ uint32_t div_by(int g) { return (65536u + (uint32_t)g - 1u) / (uint32_t)g; }
+__device__ __forceinline__ int row_token(int r, uint32_t m) { return (int)(((uint32_t)r * m) >> 16); }
+
 // Four (or two) consecutive final-output values at element offset off: fp32, or bf16 pairs
 // rounded to nearest even when the problem asks for a bf16 output.
 __device__ __forceinline__ void store_out4(const Problem& p, size_t off, float4 v) {
@@ -236,6 +254,48 @@ __device__ __forceinline__ unsigned long long tree_mask(const Problem& p, int n,
     u = up;
   }
   return m;
+}
+
+// The same for all rows of sequence n, by one warp in scratch of its own: up[t] becomes kRoot, or
+// kAbsent for an absent row, and sees[t] (where given) the mask of row t over block rows
+// [first, first + 64).  sees[t] holds the path from t up to, not including, up[t]; joining the path of
+// up[t] to it doubles its length, and since parents come before their children, rows 32 at a time
+// in order need at most 6 such steps each: 0.3 us where S <= 64, against 2.7 us for a walk up a
+// 64-long chain.
+constexpr short kRoot = -1, kAbsent = -2;
+__device__ __forceinline__ void tree_rows(const Problem& p, int n, int first, int lane, short* up,
+                                          unsigned long long* sees) {
+  const int* par = p.parents + (size_t)n * p.S;
+  __syncwarp();
+  for (int t = lane; t < p.S; t += 32) {
+    int u = __ldg(par + t);
+    if (u >= t || u < kAbsent) {
+      raise_error(p.err_word, kErrDeviceArg);
+      u = kAbsent;
+    }
+    up[t] = (short)u;
+    if (sees) sees[t] = t >= first && t < first + 64 ? 1ull << (t - first) : 0ull;
+  }
+  __syncwarp();
+  for (int t0 = 0; t0 < p.S; t0 += 32) {
+    const int t = t0 + lane;
+    int u = t < p.S ? up[t] : kRoot;
+    while (__any_sync(0xffffffffu, u >= 0)) {
+      unsigned long long m = 0ull;
+      int v = u;
+      if (u >= 0) {
+        if (sees) m = sees[u];
+        v = up[u];
+      }
+      __syncwarp();
+      if (u >= 0) {
+        if (sees) sees[t] |= m;
+        up[t] = (short)v;
+      }
+      u = v;
+      __syncwarp();
+    }
+  }
 }
 // The visible keys of a loaded tile without a tree: [head, count).
 __device__ __forceinline__ unsigned long long span_mask(int head, int count) {
