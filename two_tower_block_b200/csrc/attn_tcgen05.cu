@@ -122,11 +122,11 @@ static_assert(sizeof(Bars) + sizeof(Shared) <= 896, "barrier block overflows its
 // it (`k`, read at the start).  For each cut unit with a
 // segment in this range (at most two: the unit holding the range's first tile and the one
 // holding its last), the CTA waits until every range of that unit has reached the count,
-// then combines its share of the unit's rows: rows [i R / n, (i + 1) R / n) for the i-th of the
-// unit's n ranges, one warp per row.  No CTA waits for ranges outside its units.  The waits
+// then combines its share of the unit's items (combine_row.cuh): the i-th of n equal parts for the
+// i-th of the unit's n ranges.  No CTA waits for ranges outside its units.  The waits
 // are bounded; a CTA that gave up (or whose pipeline aborted) combines nothing and the error
 // word says so.
-template <int D, int THREADS, int PARTS, int ROWS>   // partials of a row, and rows, in flight per warp
+template <int D, int THREADS>
 __device__ __forceinline__ void fused_combine(const Problem& p, long long T, long long start, long long end,
                                               const Unit& first, const Unit& last, unsigned k, bool aborted) {
   __shared__ int s_ok;
@@ -136,6 +136,7 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
   if (tid == 0) red_release_gpu_add(p.arrivals + c, 1u);
   if (start >= end || aborted) return;
   const int Ce = used_ranges(T, p.C);
+#pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const Unit& x = which == 0 ? first : last;
     if (which == 1 && last.u == first.u) break;
@@ -144,10 +145,10 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const int c0 = range_of_tile_tab(tab, T, Ce, first_tile(x)), c1 = range_of_tile_tab(tab, T, Ce, end_tile(x) - 1);
     if (warp == 0) {
       bool ok = true;
-      const unsigned long long t0 = globaltimer_ns();
+      const unsigned long long t0 = timer_start();
       for (int cc = c0 + lane; cc <= c1 && ok; cc += 32) {
         while (ld_acquire_gpu_u32(p.arrivals + cc) < k) {
-          if (globaltimer_ns() - t0 > p.wait_limit_ns) {
+          if (timer_over(t0, p.wait_limit_ns)) {
             raise_error(p.err_word, kErrTimeout);
             ok = false;
             break;
@@ -161,9 +162,9 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     if (!s_ok) return;
     const int n = c1 - c0 + 1, i = c - c0;
     const SplitRecord rec{x.u, c1, first_after(x, range_start_tab(tab, T, Ce, c0)) ? 0 : 1, 0};
-    const int r0 = (int)((long long)i * p.R / n), r1 = (int)((long long)(i + 1) * p.R / n);
-    constexpr int kWarps = THREADS / 32;
-    for (int r = r0 + warp; r < r1; r += ROWS * kWarps) combine_rows<D, PARTS, ROWS>(p, x, c0, rec, r, kWarps, r1, lane);
+    const int items = combine_items<D>(p), share = ceil_div(items, n);
+#pragma unroll 1
+    for (int it = i * share + tid; it < min(items, (i + 1) * share); it += THREADS) combine_item<D>(p, x, c0, rec, it);
   }
 }
 
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
             zero = span_mask(0, round16(tk.count)) & ~span_mask(tk.head, tk.count);
             if (tk.is_blk && p.parents) {
               short* up = reinterpret_cast<short*>(smem + C::kTreeOff);
-              if (tk.first == 0) tree_rows(p, x.n, 0, lane, up, nullptr);
+              if (i == sg.lo) tree_rows(p, x.n, 0, lane, up, nullptr);   // (a segment may begin past tile 0)
 #pragma unroll
               for (int w = 0; w < 2; ++w) {
                 const int t = 32 * w + lane;
@@ -787,16 +788,18 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         const bool none = VIS && (absent || l == 0.f);   // no visible key: 0, lse = -inf
         const float inv = none ? 0.f : 1.f / l;
         const int rbase = m * 128 + q4 * 32;  // first packed row of this warp
-        // element offsets of the rows that this lane stores (every fourth) from the unit's first row in
-        // the output, or the segment's in the partials
-        const size_t at0 = (sg.full ? ((size_t)x.ns * p.S * p.Hq + x.h * p.g) * D : (size_t)sg.slot * p.R * D) + (lane & 7) * 4;
+        // element offsets of the rows that this lane stores of a final output (every fourth) from the
+        // unit's first row
+        const size_t at0 = ((size_t)x.ns * p.S * p.Hq + x.h * p.g) * D + (lane & 7) * 4;
         int at[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int gr = min(rbase + k * 4 + (lane >> 3), p.R - 1);
           const int t = row_token(gr, gm);
-          at[k] = (sg.full ? t * p.Hq + (gr - t * p.g) : gr) * D;
+          at[k] = (t * p.Hq + (gr - t * p.g)) * D;
         }
+        float* part = p.part_o + part_at(p, sg.slot, r, 0, D);   // four columns on: 4 R floats further
+#pragma unroll 1   // (cold code: fetched once, not four times)
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tmem_ld32(o_addr + cc * 32, o);
@@ -809,24 +812,28 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
+          auto four = [&](int q) {
+            return make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
+                               __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+          };
+          if (!sg.full) {
+            if (r < p.R) {
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<float4*>(part + (size_t)(cc * 8 + q) * 4 * p.R) = four(q);
+            }
+            continue;
+          }
           // stage the 32x32 block (16-byte chunks XOR-swizzled by row) for coalesced stores
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            float4 f = make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                                   __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
-            reinterpret_cast<float4*>(stage + lane * 32)[q ^ (lane & 7)] = f;
-          }
+          for (int q = 0; q < 8; ++q) reinterpret_cast<float4*>(stage + lane * 32)[q ^ (lane & 7)] = four(q);
           __syncwarp();
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const int rr = k * 4 + (lane >> 3);  // row within the warp's 32
             const int q = lane & 7;
-            const int gr = rbase + rr;
-            if (gr < p.R) {
-              float4 f = reinterpret_cast<const float4*>(stage + rr * 32)[q ^ (rr & 7)];
-              if (sg.full) store_out4(p, at0 + at[k] + cc * 32, f);
-              else *reinterpret_cast<float4*>(p.part_o + at0 + at[k] + cc * 32) = f;
-            }
+            if (rbase + rr < p.R)
+              store_out4(p, at0 + at[k] + cc * 32, reinterpret_cast<const float4*>(stage + rr * 32)[q ^ (rr & 7)]);
           }
           __syncwarp();
         }
@@ -865,8 +872,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (p.arrivals != nullptr)
-    fused_combine<D, kThreads, C::kSplitRegs ? 8 : 12, C::kSplitRegs ? 1 : 2>(p, T, start, end, sh->first, sh->last, sh->arrival,
-                                               *(volatile int*)&sh->abort_flag != 0);
+    fused_combine<D, kThreads>(p, T, start, end, sh->first, sh->last, sh->arrival,
+                               *(volatile int*)&sh->abort_flag != 0);
 }
 
 template <int D, int NK, bool VIS = false, bool MX = false>

@@ -537,7 +537,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(rank == 0 ? bar(bars->o_empty) : bar(bars->o_done[w]));  // O read
         }
         if (r < p.R) {
-          float* dst = out_row(p, x, sg, r, kD) + col;
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
             float4 f;
@@ -546,7 +545,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             f.y = (hasA ? wA * __uint_as_float(oa[k + 1]) : 0.f) + (hasB ? wB * __uint_as_float(ob[k + 1]) : 0.f);
             f.z = (hasA ? wA * __uint_as_float(oa[k + 2]) : 0.f) + (hasB ? wB * __uint_as_float(ob[k + 2]) : 0.f);
             f.w = (hasA ? wA * __uint_as_float(oa[k + 3]) : 0.f) + (hasB ? wB * __uint_as_float(ob[k + 3]) : 0.f);
-            *reinterpret_cast<float4*>(dst + k) = f;
+            *reinterpret_cast<float4*>(out_at(p, x, sg, r, col + k, kD)) = f;
           }
         }
       }

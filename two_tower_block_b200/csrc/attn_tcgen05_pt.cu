@@ -444,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 4
         for (int k = 0; k < 32; ++k) {
           const int row = col + k;
-          if (row < p.R) out_row(p, x, sg, row, kD)[d] = __uint_as_float(o[k]) * inv_l[row];
+          if (row < p.R) *out_at(p, x, sg, row, d, kD) = __uint_as_float(o[k]) * inv_l[row];
         }
       }
       mbar_arrive(smem_u32(&bars->epi_b));  // inv_l read by all before P is rewritten

@@ -1,5 +1,5 @@
 // Log-sum-exp combine of the units that a range boundary cut into segments
-// (combine_row.cuh: one warp per row), and the bounded-wait self test.
+// (combine_row.cuh: one thread per four columns of a row), and the bounded-wait self test.
 #include "combine_row.cuh"
 #include "problem.h"
 #include "ptx.cuh"
@@ -8,7 +8,6 @@
 namespace tt {
 namespace {
 
-constexpr int kRowsPerBlock = 8;   // one warp per row
 constexpr int kThreads = 256;
 
 template <int D>
@@ -21,10 +20,9 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
   const int c = blockIdx.x;
   const SplitRecord rec = p.records[c];
   if (rec.unit < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.y * kRowsPerBlock + warp;
-  if (r >= p.R) return;
-  combine_rows<D, 8, 1>(p, make_unit(p, rec.unit, 0), c, rec, r, 1, r + 1, lane);
+  const int item = blockIdx.y * kThreads + threadIdx.x;
+  if (item >= combine_items<D>(p)) return;
+  combine_item<D>(p, make_unit(p, rec.unit, 0), c, rec, item);
 }
 
 // One thread waits on a barrier that nothing arrives at; the bounded wait must
@@ -68,7 +66,7 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   // a programmatic dependent launch: the launch overlaps the attention kernel's tail and the
   // kernel waits for the attention grid on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.C, (p.R + kRowsPerBlock - 1) / kRowsPerBlock, 1);
+  cfg.gridDim = dim3(p.C, (p.R * (p.D / 4) + kThreads - 1) / kThreads, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -56,7 +56,7 @@ struct Problem {
   const long long* causal_starts;  // block-causal: range boundary table (min(C, T) + 1 entries) or
                                    // null for the uniform split
   // plan-owned scratch
-  float* part_o;        // [2C][R][D]
+  float* part_o;        // [2C][D / 4][R][4] (walker.cuh: part_at)
   float* part_lse;      // [2C][R]
   SplitRecord* records; // [C]
   unsigned* err_word;

@@ -21,6 +21,21 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
+// The start of a bounded wait, and whether it has run past its limit.  Nothing promises that the two
+// halves of the timer are read at once: a read across a carry may be 4.3 s off, so the start is taken
+// from two reads that agree, and the limit must be seen passed twice.
+__device__ __forceinline__ unsigned long long timer_start() {
+  unsigned long long a = globaltimer_ns(), b = globaltimer_ns();
+  for (int k = 0; k < 4 && b - a > 1000000ull; ++k) {
+    a = b;
+    b = globaltimer_ns();
+  }
+  return b;
+}
+__device__ __forceinline__ bool timer_over(unsigned long long t0, unsigned long long limit_ns) {
+  return (long long)(globaltimer_ns() - t0) > (long long)limit_ns &&
+         (long long)(globaltimer_ns() - t0) > (long long)limit_ns;
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -136,12 +151,12 @@ struct WaitCtx {
 // ran past its limit, in which case it raises kErrTimeout and aborts the CTA.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
   if (mbar_try_wait(bar, parity)) return true;
-  unsigned long long t0 = globaltimer_ns();
+  const unsigned long long t0 = timer_start();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
     if ((it & 15u) == 0u) {
       if (*w.abort_flag) return false;
-      if (globaltimer_ns() - t0 > w.limit_ns) {
+      if (timer_over(t0, w.limit_ns)) {
         raise_error(w.err_word, kErrTimeout);
         *w.abort_flag = 1;
         return false;
@@ -350,12 +365,12 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // Bounded wait with acquire at cluster scope (for barriers other CTAs arrive on).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  unsigned long long t0 = globaltimer_ns();
+  const unsigned long long t0 = timer_start();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 15u) == 0u) {
       if (*w.abort_flag) return false;
-      if (globaltimer_ns() - t0 > w.limit_ns) {
+      if (timer_over(t0, w.limit_ns)) {
         raise_error(w.err_word, kErrTimeout);
         *w.abort_flag = 1;
         return false;

@@ -10,13 +10,10 @@ namespace tt {
 
 __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; }
 
-// Output row pointer of packed row r of unit x (final output or segment partial).
-__device__ __forceinline__ float* out_row(const Problem& p, const Unit& x, const Segment& sg, int r, int D) {
-  if (sg.full) {
-    const int t = r / p.g, j = r - (r / p.g) * p.g;
-    return p.out + ((size_t)(x.ns * p.S + t) * p.Hq + x.h * p.g + j) * D;
-  }
-  return p.part_o + ((size_t)sg.slot * p.R + r) * D;
+// Column col of packed row r of unit x (final output or segment partial); up to four columns from a
+// multiple of four lie together.
+__device__ __forceinline__ float* out_at(const Problem& p, const Unit& x, const Segment& sg, int r, int col, int D) {
+  return sg.full ? p.out + out_offset(p, x, r, D) + col : p.part_o + part_at(p, sg.slot, r, col, D);
 }
 
 // Two non-negative finite weights rounded to bf16 precision on the integer pipe (round half

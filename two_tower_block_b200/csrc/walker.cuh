@@ -81,6 +81,7 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
   int cost = 0, t = 0;   // t: tiles of a unit of sequence base + lane (total rows < 2^31: sums fit)
   if (p.mode == kDecode) {
     int tot = 0, least = INT32_MAX, most = 0;
+#pragma unroll 1   // (cold code: short, or its instruction fetches are what a small call waits for)
     for (int base = 0; base < p.B; base += 32) {
       const int n = base + lane;
       t = n < p.B ? unit_tiles_k(p, clamp_len(p, n, c == 0)) : 0;
@@ -106,6 +107,7 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
   end = range_start_tab(tab, T, Ce, c + 1);
   if (p.mode == kDecode) {
     long long acc = 0;
+#pragma unroll 1
     for (int base = 0; base < p.B; base += 32) {
       const int n = base + lane;
       if (p.B > 32) t = n < p.B ? unit_tiles_k(p, clamp_len(p, n, false)) : 0;
@@ -183,6 +185,12 @@ __device__ __forceinline__ SplitRecord record_of(const Unit& last, long long T, 
 __device__ __forceinline__ size_t out_offset(const Problem& p, const Unit& x, int r, int D) {
   const int t = r / p.g, j = r - (r / p.g) * p.g;
   return ((size_t)(x.ns * p.S + t) * p.Hq + x.h * p.g + j) * D;
+}
+// Element offset of columns [col, col + 4) (col a multiple of 4) of packed row r in partial slot `slot`.
+// Four columns of consecutive rows lie together: a warp whose lanes hold rows writes 512 bytes at a
+// time straight from its registers, and a combining warp reads them so.
+__device__ __forceinline__ size_t part_at(const Problem& p, int slot, int r, int col, int D) {
+  return (((size_t)slot * (D / 4) + col / 4) * p.R + r) * 4 + (col & 3);
 }
 // r / g for packed rows r < 256 of a unit (g <= 256): with m = ceil(2^16 / g) the product r m exceeds
 // r 2^16 / g by less than 2^8 <= 2^16 / g.
