@@ -9,6 +9,7 @@ no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -162,26 +163,28 @@ def _args(device, *items):
         _arg(t, name, numel, kind, device)
 
 
-# The type each kind of argument usually has; _addrs takes these without a further look.
+# The type each kind of argument usually has.
 _USUAL = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
           "e4m3": torch.float8_e4m3fn}
 
 
+def _quick(device, tensors, want):
+    """Addresses of tensors that are all of the usual type, the right size, contiguous and on the device:
+    one look at each, since a small call's host time is what it waits for.  ``want``: (dtype, numel) of
+    each.  None if one is not (or is no tensor): _addrs then says what is wrong, or takes it."""
+    at = []
+    try:
+        for t, (dtype, numel) in zip(tensors, want):
+            if t.dtype is not dtype or t.numel() != numel or t.get_device() != device or not t.is_contiguous():
+                return None
+            at.append(t.data_ptr())
+    except AttributeError:
+        return None
+    return at
+
+
 def _addrs(device, items):
-    """Addresses of (tensor, name, numel, kind) items after the checks of _args.  A call's host time is
-    what a small decode waits for, so tensors of the usual type that pass are looked at once, with
-    the fewest calls into torch; whatever does not goes through _args, which says what is wrong."""
-    found = []
-    for t, _, numel, kind in items:
-        if t is None:
-            found.append(None)
-        elif (t.__class__ is torch.Tensor and t.dtype is _USUAL[kind] and t.numel() == numel
-              and t.get_device() == device and t.is_contiguous()):
-            found.append(t.data_ptr())
-        else:
-            break
-    else:
-        return found
+    """Addresses of (tensor, name, numel, kind) items after the checks of _args."""
     _args(device, *items)
     return [_ptr(t) for t, _, _, _ in items]
 
@@ -229,7 +232,9 @@ class MxCache:
             items.append((page_table, "page_table", page_table.numel(), "i32"))
         self.device = k.device
         # (a device cache's tensors are all on that device; a host one is refused by the calls)
-        at = _addrs(k.get_device() if k.is_cuda else None, items)
+        dev = k.get_device() if k.is_cuda else None
+        at = _quick(dev, [t for t, _, _, _ in items], [(_USUAL[kind], m) for _, _, m, kind in items]) or \
+            _addrs(dev, items)
         self._d = MxCacheDesc(at[0], at[1], at[2], at[3], at[4] if page_table is not None else None, num_pages,
                               page_size, pages_per_seq)
         self._ref = ctypes.byref(self._d)
@@ -296,15 +301,45 @@ class Plan:
         return inf
 
     # --- decode ------------------------------------------------------------
-    # Each call lists its tensors in the C function's order of checks, and hands the addresses on.
+    # Each call hands the addresses of its tensors on: by _quick, or where that finds something to look
+    # at, by the checks of _addrs in their order (every size and type first, then every device).
     def _outputs(self, q, out, lse, want_lse, tokens):
         """out and lse as given, or new ones ([B, tokens, Hq, D], and [B, Hq, tokens] where wanted)."""
         s = self.shape
         if out is None:
-            out = torch.empty((s.batch, tokens, s.q_heads, s.head_dim), dtype=self.out_dtype, device=q.device)
+            shape = (s.batch, tokens, s.q_heads, s.head_dim)
+            if q.dtype is self.out_dtype and q.shape == shape and q.is_contiguous():
+                out = torch.empty_like(q)
+            else:
+                out = torch.empty(shape, dtype=self.out_dtype, device=q.device)
         if lse is None and want_lse:
             lse = torch.empty((s.batch, s.q_heads, tokens), dtype=torch.float32, device=q.device)
         return out, lse
+
+    @functools.cached_property
+    def _usual(self):
+        """What _quick wants of a decode call's tensors: q, k_blk, v_blk, ctx_lens, out; k_ctx and v_ctx;
+        parents; lse."""
+        s = self.shape
+        rows = s.batch * s.block
+        nq, nb = rows * s.q_heads * s.head_dim, rows * s.kv_heads * s.head_dim
+        nc = s.batch * s.kv_heads * s.ctx_capacity * s.head_dim
+        b, i = torch.bfloat16, torch.int32
+        return (((b, nq), (b, nb), (b, nb), (i, s.batch), (self.out_dtype, nq)), ((b, nc), (b, nc)), ((i, rows),),
+                ((torch.float32, rows * s.q_heads),))
+
+    def _decode_args(self, q, k_blk, v_blk, ctx_lens, out, lse, more, want, items):
+        """Addresses of q, k_blk, v_blk, ctx_lens, out, lse and then of ``more`` (wanted as ``want``;
+        ``items`` gives the same for _addrs)."""
+        usual = self._usual
+        first = (q, k_blk, v_blk, ctx_lens, out)
+        if lse is None:
+            at = _quick(self.device, first + more, usual[0] + want)
+            if at is not None:
+                at.insert(5, None)
+        else:
+            at = _quick(self.device, first + (lse,) + more, usual[0] + usual[3] + want)
+        return at or _addrs(self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + items())
 
     def _decode_items(self, q, k_blk, v_blk, ctx_lens, out, lse):
         s = self.shape
@@ -320,7 +355,7 @@ class Plan:
         return (k_ctx, "k_ctx", nc, "bf16"), (v_ctx, "v_ctx", nc, "bf16")
 
     def _page_items(self, k_pages, v_pages, page_table):
-        """(num_pages, page_size, pages_per_seq, items to check) of a paged context."""
+        """(num_pages, page_size, pages_per_seq, items to check, what _quick wants) of a paged context."""
         s = self.shape
         if k_pages is None:
             num_pages, page_size = 0, 16      # no pool: valid only without context (the library checks)
@@ -335,9 +370,10 @@ class Plan:
             if page_table.dim() != 2 or page_table.shape[0] != s.batch:
                 raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [{s.batch}, pages_per_seq]")
             pages_per_seq = page_table.shape[1]
-        return int(num_pages), int(page_size), int(pages_per_seq), (
+        return int(num_pages), int(page_size), int(pages_per_seq), lambda: (
             (k_pages, "k_pages", pool_numel, "bf16"), (v_pages, "v_pages", pool_numel, "bf16"),
-            (page_table, "page_table", s.batch * pages_per_seq, "i32"))
+            (page_table, "page_table", s.batch * pages_per_seq, "i32")), (
+            (torch.bfloat16, pool_numel), (torch.bfloat16, pool_numel), (torch.int32, s.batch * pages_per_seq))
 
     def _parents_item(self, parents):
         return (parents, "parents", self.shape.batch * self.shape.block, "i32")
@@ -351,8 +387,9 @@ class Plan:
     def block_attn(self, q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out=None, lse=None, stream=None,
                    want_lse=False):
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
-        q_, kb, vb, lens, o, l, kc, vc = _addrs(self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse)
-                                                + self._slab_items(k_ctx, v_ctx))
+        q_, kb, vb, lens, o, l, kc, vc = self._decode_args(
+            q, k_blk, v_blk, ctx_lens, out, lse, (k_ctx, v_ctx), self._usual[1],
+            lambda: self._slab_items(k_ctx, v_ctx))
         _check(lib().tt_block_attn(self._h, q_, kc, vc, kb, vb, lens, o, l, self._on(stream)), "tt_block_attn")
         return (out, lse) if lse is not None else out
 
@@ -362,9 +399,9 @@ class Plan:
         pools, page_table [B, pages_per_seq] int32 (device); P = k_pages.shape[2].  With no
         context at all, the pools and the table may be None."""
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
-        num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
-        q_, kb, vb, lens, o, l, kp, vp, tab = _addrs(
-            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + items)
+        num_pages, page_size, pages_per_seq, items, want = self._page_items(k_pages, v_pages, page_table)
+        q_, kb, vb, lens, o, l, kp, vp, tab = self._decode_args(
+            q, k_blk, v_blk, ctx_lens, out, lse, (k_pages, v_pages, page_table), want, items)
         _check(lib().tt_block_attn_paged(self._h, q_, kp, vp, tab, num_pages, page_size, pages_per_seq, kb, vb, lens,
                                          o, l, self._on(stream)), "tt_block_attn_paged")
         return (out, lse) if lse is not None else out
@@ -374,9 +411,9 @@ class Plan:
         """Decode whose block is a tree of drafted tokens: parents [B, S] int32 (-1: hangs on the last
         committed token, -2: absent).  Otherwise as block_attn."""
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
-        q_, kb, vb, lens, o, l, kc, vc, par = _addrs(
-            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + self._slab_items(k_ctx, v_ctx)
-            + (self._parents_item(parents),))
+        q_, kb, vb, lens, o, l, kc, vc, par = self._decode_args(
+            q, k_blk, v_blk, ctx_lens, out, lse, (k_ctx, v_ctx, parents), self._usual[1] + self._usual[2],
+            lambda: self._slab_items(k_ctx, v_ctx) + (self._parents_item(parents),))
         _check(lib().tt_block_attn_tree(self._h, q_, kc, vc, kb, vb, lens, par, o, l, self._on(stream)),
                "tt_block_attn_tree")
         return (out, lse) if lse is not None else out
@@ -385,10 +422,10 @@ class Plan:
                               lse=None, stream=None, want_lse=False):
         """block_attn_tree over a paged context cache (pages as block_attn_paged)."""
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
-        num_pages, page_size, pages_per_seq, items = self._page_items(k_pages, v_pages, page_table)
-        q_, kb, vb, lens, o, l, kp, vp, tab, par = _addrs(
-            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + items
-            + (self._parents_item(parents),))
+        num_pages, page_size, pages_per_seq, items, want = self._page_items(k_pages, v_pages, page_table)
+        q_, kb, vb, lens, o, l, kp, vp, tab, par = self._decode_args(
+            q, k_blk, v_blk, ctx_lens, out, lse, (k_pages, v_pages, page_table, parents), want + self._usual[2],
+            lambda: items() + (self._parents_item(parents),))
         _check(lib().tt_block_attn_tree_paged(self._h, q_, kp, vp, tab, num_pages, page_size, pages_per_seq, kb, vb,
                                               lens, par, o, l, self._on(stream)), "tt_block_attn_tree_paged")
         return (out, lse) if lse is not None else out
@@ -398,11 +435,27 @@ class Plan:
                       want_lse=False):
         """Decode over a quantised context cache (MxCache); with ``parents`` the block is a drafted tree."""
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.block)
-        q_, kb, vb, lens, o, l, par = _addrs(
-            self.device, self._decode_items(q, k_blk, v_blk, ctx_lens, out, lse) + (self._parents_item(parents),))
-        _check(lib().tt_block_attn_mx(self._h, q_, cache._fits(self), kb, vb, lens, par, o, l, self._on(stream)),
+        tree = parents is not None
+        q_, kb, vb, lens, o, l, *par = self._decode_args(
+            q, k_blk, v_blk, ctx_lens, out, lse, (parents,) if tree else (), self._usual[2] if tree else (),
+            lambda: (self._parents_item(parents),) if tree else ())
+        _check(lib().tt_block_attn_mx(self._h, q_, cache._fits(self), kb, vb, lens, par[0] if tree else None,
+                                      o, l, self._on(stream)),
                "tt_block_attn_mx")
         return (out, lse) if lse is not None else out
+
+    def _rows_args(self, k, v, n, ctx_lens, per_seq, names):
+        """Addresses of the rows k and v of n elements each, ctx_lens, and one optional int32 per sequence."""
+        B = self.shape.batch
+        want = (torch.bfloat16, n), (torch.bfloat16, n), (torch.int32, B), (torch.int32, B)
+        if per_seq is not None:
+            at = _quick(self.device, (k, v, ctx_lens, per_seq), want)
+        else:
+            at = _quick(self.device, (k, v, ctx_lens), want[:3])
+            if at is not None:
+                at.append(None)
+        return at or _addrs(self.device, ((k, names[0], n, "bf16"), (v, names[1], n, "bf16"),
+                                          (ctx_lens, "ctx_lens", B, "i32"), (per_seq, names[2], B, "i32")))
 
     def kv_append_mx(self, k_new, v_new, cache, ctx_lens, counts=None, advance=True, stream=None):
         """Quantise k_new/v_new [B, rows, Hkv, D] into the cache at [L_n, L_n + counts[n]) (all rows
@@ -412,9 +465,7 @@ class Plan:
             raise ValueError(f"k_new: shape {tuple(k_new.shape)}, expected [{s.batch}, rows, {s.kv_heads}, "
                              f"{s.head_dim}]")
         n = k_new.numel()
-        kn, vn, lens, cnt = _addrs(self.device, ((k_new, "k_new", n, "bf16"), (v_new, "v_new", n, "bf16"),
-                                                 (ctx_lens, "ctx_lens", s.batch, "i32"),
-                                                 (counts, "counts", s.batch, "i32")))
+        kn, vn, lens, cnt = self._rows_args(k_new, v_new, n, ctx_lens, counts, ("k_new", "v_new", "counts"))
         _check(lib().tt_kv_append_mx(self._h, kn, vn, k_new.shape[1], cnt, cache._fits(self), lens,
                                      int(bool(advance)), self._on(stream)), "tt_kv_append_mx")
 
@@ -426,9 +477,7 @@ class Plan:
             raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [{s.batch}, {s.kv_heads}, rows, "
                              f"{s.head_dim}]")
         n = k_out.numel()
-        ko, vo, lens, st = _addrs(self.device, ((k_out, "k_out", n, "bf16"), (v_out, "v_out", n, "bf16"),
-                                                (ctx_lens, "ctx_lens", s.batch, "i32"),
-                                                (starts, "starts", s.batch, "i32")))
+        ko, vo, lens, st = self._rows_args(k_out, v_out, n, ctx_lens, starts, ("k_out", "v_out", "starts"))
         _check(lib().tt_kv_read_mx(self._h, cache._fits(self), lens, st, k_out.shape[2], ko, vo, self._on(stream)),
                "tt_kv_read_mx")
         return k_out, v_out
