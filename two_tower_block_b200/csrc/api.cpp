@@ -609,7 +609,8 @@ tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int
   }
   P->causal_pref = pref.empty() ? nullptr : reinterpret_cast<int*>(w + b_po + b_pl + b_rec + b_err);
   P->causal_starts = tab.empty() ? nullptr : reinterpret_cast<long long*>(w + b_po + b_pl + b_rec + b_err + b_pref + b_arr);
-  e = cudaMemset(P->err_word, 0, b_err);
+  if (P->kernel == TT_KERNEL_TCGEN05) e = tt::prepare_attn_tcgen05(d.head_dim, P->R);
+  if (e == cudaSuccess) e = cudaMemset(P->err_word, 0, b_err);
   if (e == cudaSuccess) e = cudaMemset(P->arr_decode, 0, b_arr);
   if (e == cudaSuccess && !pref.empty())
     e = cudaMemcpy(P->causal_pref, pref.data(), pref.size() * sizeof(int), cudaMemcpyHostToDevice);

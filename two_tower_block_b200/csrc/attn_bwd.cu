@@ -22,6 +22,7 @@
 
 #include "errbits.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "sched.cuh"
 
 namespace tt {
@@ -293,13 +294,11 @@ constexpr size_t smem_bytes() {
 }  // namespace
 
 cudaError_t launch_attn_bwd(const BwdProblem& p, cudaStream_t stream) {
-  static const bool attr_done = [] {
-    cudaFuncSetAttribute(attn_bwd_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem_bytes<128>());
-    cudaFuncSetAttribute(attn_bwd_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<64>());
-    return true;
-  }();
-  (void)attr_done;
+  static std::atomic<unsigned long long> done[2];
+  const cudaError_t e =
+      p.D == 128 ? smem_opt_in(reinterpret_cast<const void*>(&attn_bwd_kernel<128>), (int)smem_bytes<128>(), done[1])
+                 : smem_opt_in(reinterpret_cast<const void*>(&attn_bwd_kernel<64>), (int)smem_bytes<64>(), done[0]);
+  if (e != cudaSuccess) return e;
   const dim3 grid(p.B * p.Hkv * p.NB, (p.R + kRows - 1) / kRows);
   if (p.D == 128) attn_bwd_kernel<128><<<grid, kThreads, smem_bytes<128>(), stream>>>(p);
   else attn_bwd_kernel<64><<<grid, kThreads, smem_bytes<64>(), stream>>>(p);

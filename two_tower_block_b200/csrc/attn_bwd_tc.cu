@@ -39,6 +39,7 @@
 
 #include "errbits.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "sched.cuh"
 
 namespace tt {
@@ -598,14 +599,11 @@ bool attn_bwd_tc_supported(const BwdProblem& p) {
 size_t attn_bwd_tc_smem_bytes(int D) { return D == 128 ? BwdCfg<128>::kSmemBytes : BwdCfg<64>::kSmemBytes; }
 
 cudaError_t launch_attn_bwd_tc(const BwdProblem& p, const BwdMaps& maps, int num_ctas, cudaStream_t stream) {
-  static const bool attr_done = [] {
-    cudaFuncSetAttribute(attn_bwd_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         BwdCfg<128>::kSmemBytes);
-    cudaFuncSetAttribute(attn_bwd_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         BwdCfg<64>::kSmemBytes);
-    return true;
-  }();
-  (void)attr_done;
+  static std::atomic<unsigned long long> done[2];
+  const cudaError_t opt =
+      p.D == 128 ? smem_opt_in(reinterpret_cast<const void*>(&attn_bwd_tc_kernel<128>), BwdCfg<128>::kSmemBytes, done[1])
+                 : smem_opt_in(reinterpret_cast<const void*>(&attn_bwd_tc_kernel<64>), BwdCfg<64>::kSmemBytes, done[0]);
+  if (opt != cudaSuccess) return opt;
   const int MT = p.R > 128 ? 2 : 1;
   const long long items = (long long)p.B * p.Hkv * p.NB * MT;
   const int grid = (int)(items < num_ctas ? items : num_ctas);

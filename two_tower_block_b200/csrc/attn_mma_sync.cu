@@ -14,6 +14,7 @@
 #include "mx.cuh"
 #include "problem.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "walker.cuh"
 
 namespace tt {
@@ -300,22 +301,17 @@ size_t attn_mma_sync_smem_bytes(int D) { return (size_t)(kRows + 4 * kKeys) * (D
 cudaError_t launch_attn_mma_sync(const Problem& p, cudaStream_t stream) {
   const size_t smem = attn_mma_sync_smem_bytes(p.D);
   dim3 grid(p.C, (p.R + kRows - 1) / kRows);
-  // The opt-in shared-memory size is set once per process (not during a graph capture).
   using Kernel = void (*)(const Problem);
   static const Kernel table[2][2][2] = {   // [head_dim 128][tree][mx]
       {{attn_mma_sync_kernel<64, false, false>, attn_mma_sync_kernel<64, false, true>},
        {attn_mma_sync_kernel<64, true, false>, attn_mma_sync_kernel<64, true, true>}},
       {{attn_mma_sync_kernel<128, false, false>, attn_mma_sync_kernel<128, false, true>},
        {attn_mma_sync_kernel<128, true, false>, attn_mma_sync_kernel<128, true, true>}}};
-  static const bool attr_done = [] {
-    for (int d = 0; d < 2; ++d)
-      for (int k = 0; k < 4; ++k)
-        cudaFuncSetAttribute(table[d][k >> 1][k & 1], cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)attn_mma_sync_smem_bytes(d ? 128 : 64));
-    return true;
-  }();
-  (void)attr_done;
-  const Kernel k = table[p.D == 128][p.parents != nullptr][p.k_scale != nullptr];
+  static std::atomic<unsigned long long> done[2][2][2];
+  const int d = p.D == 128, t = p.parents != nullptr, m = p.k_scale != nullptr;
+  const Kernel k = table[d][t][m];
+  const cudaError_t e = smem_opt_in(reinterpret_cast<const void*>(k), (int)smem, done[d][t][m]);
+  if (e != cudaSuccess) return e;
   k<<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }

@@ -46,6 +46,12 @@
 // (load_raw_tiles), four more warps (12..15) write them as bf16 into the ring (convert_tiles), and
 // warp 0 keeps Q and both of the block's own tiles.
 //
+// SPLIT (units of at most 128 rows): one M-tile leaves half of the roles idle while the softmax of one tile
+// after another bounds the kernel (0.95 us a tile, against 0.75 us that HBM needs for it).  The two
+// MMA warps and softmax warpgroups then share the unit's tiles, even ones to the first and
+// odd ones to the second, each with its own accumulator; at the end both read both accumulators,
+// half of the columns each, and weigh them by e^(m - max) as the combine does.
+//
 // Every wait is bounded (ptx.cuh: mbar_wait); on a timeout the CTA raises the
 // error word, drains what it issued, frees TMEM and returns.
 #include <type_traits>
@@ -54,6 +60,7 @@
 #include "mx.cuh"
 #include "problem.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "tc_common.cuh"
 #include "walker.cuh"
 
@@ -65,14 +72,16 @@ constexpr int kRowBytes = 128;              // one 64-element bf16 row of a swiz
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr float kNoKey = -1e30f;            // reference maximum of a row that has seen no key yet
 
-template <int D, int NK, bool MX = false>
+template <int D, int NK, bool MX = false, bool SPLIT = false>
 struct Cfg {
+  static constexpr int kRows = SPLIT ? 128 : kMaxRows;          // rows of Q in shared memory
   static constexpr int kThreads = MX ? 512 : 384;
   static constexpr int kHalves = D / 64;
   static constexpr int kBufs = 128 / NK;                       // S buffers per M-tile
   static constexpr int kSlotBytes = NK * kRowBytes * kHalves;  // one K or V tile
-  static constexpr int kStages = (MX ? 64 : 128) * 1024 / kSlotBytes;  // the ring: 128 KB, or 64 KB beside raw tiles
-  static constexpr int kQBytes = kMaxRows * kRowBytes * kHalves;
+  // the ring: 128 KB, or what fits beside raw tiles
+  static constexpr int kStages = (!MX ? 128 : SPLIT ? 96 : 64) * 1024 / kSlotBytes;
+  static constexpr int kQBytes = kRows * kRowBytes * kHalves;
   static constexpr int kStageOff = kQBytes;
   static constexpr int kEpiOff = kStageOff + kStages * kSlotBytes;
   static constexpr int kEpiBytes = 8 * 32 * 32 * 4;  // 8 softmax warps x 32 rows x 32 fp32
@@ -80,7 +89,8 @@ struct Cfg {
   static constexpr int kBarBytes = 896;
   // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
   static constexpr int kTreeOff = kBarOff + kBarBytes;   // a tree's absent rows, for the V tiles
-  static constexpr int kRawOff = kTreeOff + kMaxRows * 2;
+  static constexpr int kMlOff = kTreeOff + kMaxRows * 2;   // SPLIT: (maximum, sum) of each row, [2][2][128]
+  static constexpr int kRawOff = kMlOff + (SPLIT ? 4 * 128 * 8 : 0);
   static constexpr int kRawScale = 2 * NK * D;                      // byte offsets within a slot
   static constexpr int kScaleBytes = NK * (D / kMxBlock) + 16;
   static constexpr int kRawMask = kRawScale + 2 * kScaleBytes;
@@ -95,6 +105,9 @@ struct Cfg {
   static_assert(4 * 32 * (kCtrlRegs + (MX ? kConvRegs : 0)) + 8 * 32 * kSoftmaxRegs <= kThreads * (MX ? 128 : 168),
                 "register split");
   static_assert(kStages <= 16 && kRaw <= 6, "ring too deep");
+  // SPLIT: a consumer waits for every second tile; with at least three slots each of K and V, the use
+  // before the one it waits for has always been filled (a barrier's parity tells only adjacent uses apart)
+  static_assert(!SPLIT || kStages >= 6, "ring too short for two streams");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -102,6 +115,7 @@ struct Bars {
   uint64_t q_full, q_empty, tail, drain;
   uint64_t s_full[2][2], p_full[2][2];  // [M-tile][S buffer]
   uint64_t pv_done[2], o_full[2], o_empty[2];
+  uint64_t ml_full;         // SPLIT: both warpgroups' (maximum, sum) are in shared memory
   uint64_t kv_full[16], kv_empty[16];
   uint64_t blk_go[16];      // MX: this slot is free for a block tile
   uint64_t raw_full[6], raw_empty[6];  // MX: the ring of raw tiles
@@ -172,10 +186,10 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
 // copies (the rows of a cache or of a page lie one after another), the scale bytes by four-byte
 // asynchronous copies, both counted by the slot's barrier.  One warp, which waits for nothing else, so
 // that it stays kRaw tiles ahead of the conversion across units.
-template <int D, int NK>
+template <int D, int NK, bool SPLIT>
 __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                                const WaitCtx& wc, int c, int lane) {
-  using C = Cfg<D, NK, true>;
+  using C = Cfg<D, NK, true, SPLIT>;
   constexpr int kRowScale = D / kMxBlock;
   const uint8_t* src[2] = {reinterpret_cast<const uint8_t*>(p.k_ctx), reinterpret_cast<const uint8_t*>(p.v_ctx)};
   const uint8_t* scales[2] = {p.k_scale, p.v_scale};
@@ -250,10 +264,10 @@ __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* s
 // become zeros, so P V meets no other row.  In each quarter of a warp, four lanes work on one
 // 64-element half of a row and four on the other half of the next row, which keeps both the
 // loads and the swizzled stores free of bank conflicts.
-template <int D, int NK>
+template <int D, int NK, bool SPLIT>
 __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                               const WaitCtx& wc, int c, int w, int lane) {
-  using C = Cfg<D, NK, true>;
+  using C = Cfg<D, NK, true, SPLIT>;
   constexpr int H = C::kStages / 2, kRowScale = D / kMxBlock;
   const int kv = w >> 1, first_row = 32 * (w & 1);
   const long long start = sh->start, end = sh->end;
@@ -338,10 +352,10 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
   }
 }
 
-template <int D, int NK, bool VIS, bool MX>
-__global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
+template <int D, int NK, bool VIS, bool MX, bool SPLIT>
+__global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
     attn_tcgen05_kernel(const Problem p, const __grid_constant__ TmaMaps maps) {
-  using C = Cfg<D, NK, MX>;
+  using C = Cfg<D, NK, MX, SPLIT>;
   constexpr int NBUF = C::kBufs, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -354,7 +368,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c = blockIdx.x;
-  const int MT = p.R > 128 ? 2 : 1;
+  const int MT = !SPLIT && p.R > 128 ? 2 : 1;
+  const int NS = SPLIT ? 2 : MT;        // MMA warps and softmax warpgroups at work
   // a dependent combine launch may be scheduled now; it waits for this grid on the device
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -370,9 +385,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
   }
   if (tid == 0) {
     mbar_init(smem_u32(&bars->q_full), 1);
-    mbar_init(smem_u32(&bars->q_empty), MT);  // one commit per M-tile issuer
+    mbar_init(smem_u32(&bars->q_empty), NS);  // one commit per issuer
     mbar_init(smem_u32(&bars->tail), 1);
-    mbar_init(smem_u32(&bars->drain), MT);
+    mbar_init(smem_u32(&bars->drain), NS);
+    mbar_init(smem_u32(&bars->ml_full), 256);
     for (int m = 0; m < 2; ++m) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&bars->s_full[m][b]), 1);
@@ -380,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       }
       mbar_init(smem_u32(&bars->pv_done[m]), 1);
       mbar_init(smem_u32(&bars->o_full[m]), 1);
-      mbar_init(smem_u32(&bars->o_empty[m]), 128);
+      mbar_init(smem_u32(&bars->o_empty[m]), SPLIT ? 256 : 128);
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&bars->kv_full[s]), MX ? 2 : 1);  // MX: the tile's two converter warps
@@ -436,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
   }
 
   if (MX && warp == 3 && have_work) {
-    if constexpr (MX) load_raw_tiles<D, NK>(p, sh, bars, smem, wc, c, lane);
+    if constexpr (MX) load_raw_tiles<D, NK, SPLIT>(p, sh, bars, smem, wc, c, lane);
   } else if ((warp == 0 || warp == 3) && have_work) {
     // =========================================================== producers ==
     // Warp 0 loads Q of each segment and the K tiles, warp 3 the V tiles, each into its own
@@ -458,7 +474,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           const uint32_t bar = smem_u32(&bars->q_full);
           mbar_arrive_expect_tx(bar, (uint32_t)(p.R * kRowBytes * C::kHalves));
           for (int hf = 0; hf < C::kHalves; ++hf)
-            tma_load_3d(q_s + hf * (kMaxRows * kRowBytes), &maps.q, bar, hf * 64, x.h * p.g, x.ns * p.S);
+            tma_load_3d(q_s + hf * (C::kRows * kRowBytes), &maps.q, bar, hf * 64, x.h * p.g, x.ns * p.S);
         }
         ++q_it;
       }
@@ -565,7 +581,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         for (int h = kv; h < (MX ? 2 : kv + 1); ++h) mbar_wait(smem_u32(&bars->kv_full[h * H + j % H]), (j / H) & 1, dw);
       if (q_it) mbar_wait(smem_u32(&bars->q_full), (q_it - 1) & 1, dw);
     }
-  } else if ((warp == 1 || (warp == 2 && MT == 2)) && have_work) {
+  } else if ((warp == 1 || (warp == 2 && NS == 2)) && have_work) {
     // ====================================================== MMA issuers ==
     // One warp per M-tile (warp 1: M-tile 0, warp 2: M-tile 1), so an M-tile whose P is not
     // ready never holds back the other's MMAs; the tensor core interleaves the two instruction
@@ -579,7 +595,9 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     bool ok = true;
     Unit x = sh->first;
     // descriptors: a start-address offset is added in 16-byte units to the low field
-    const uint64_t qdesc = smem_desc_sw128(q_s + m * 128 * kRowBytes, 16, 1024);
+    const uint64_t qdesc = smem_desc_sw128(q_s + (SPLIT ? 0 : m * 128 * kRowBytes), 16, 1024);
+    constexpr int kStep = SPLIT ? 2 : 1;   // of a segment's tiles, this warp's are j0, j0 + kStep, ...
+    const int j0 = SPLIT ? m : 0;
     const uint64_t kdesc0 = smem_desc_sw128(kv_s, 16, 1024);
     const uint64_t vdesc0 = smem_desc_sw128(kv_s, NK * kRowBytes, 1024);
     const uint32_t idesc_pv = idesc_bf16_f32(128, D, 0, 1);
@@ -592,7 +610,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * (kMaxRows * kRowBytes) + (kk & 3) * 32;
+          const uint32_t off = (kk >> 2) * (C::kRows * kRowBytes) + (kk & 3) * 32;
           const uint32_t koff = (kk >> 2) * (NK * kRowBytes) + (kk & 3) * 32;
           tc_mma_ss(s_tmem + buf * NK, qdesc + (off >> 4), kd + (koff >> 4), idesc, kk > 0);
         }
@@ -612,19 +630,21 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
       ++q_it;
       if (!ok) break;
       tc_fence_after();
-      // prologue: S of the segment's first NBUF tiles
-      for (int j = 0; j < NBUF && j < n && ok; ++j) {
+      // prologue: S of the warp's first NBUF tiles
+      for (int i = 0, j = j0; i < NBUF && j < n && ok; ++i, j += kStep) {
         ok = kv_wait(tb + j, 0);
         if (!ok) break;
         tc_fence_after();
-        issue_s((G + j) % NBUF, (tb + j) % H, round16(tile_keys(p, x, sg.lo + j).count));
+        issue_s((G + i) % NBUF, (tb + j) % H, round16(tile_keys(p, x, sg.lo + j).count));
       }
-      for (int j = 0; j < n && ok; ++j, ++G) {
+      // (a warp without a tile waits for its accumulator all the same: no phase may be missed)
+      if (SPLIT && ok && j0 >= n) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
+      for (int j = j0; j < n && ok; j += kStep, ++G) {
         const int b = G % NBUF;
         const uint32_t ev = H + (tb + j) % H;  // stage of V of tile j
         ok = kv_wait(tb + j, 1);
         if (ok) ok = mbar_wait_warp(smem_u32(&bars->p_full[m][b]), (G / NBUF) & 1, wc);
-        if (ok && j == 0) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
+        if (ok && j == j0) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
         if (!ok) break;
         tc_fence_after();
         const int nv = round16(tile_keys(p, x, sg.lo + j).count);
@@ -635,22 +655,23 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
 #pragma unroll
             for (int kk = 0; kk < NK / 16; ++kk)
               tc_mma_ts(o_tmem, pa + kk * 8, vd + (uint64_t)(kk * 16 * kRowBytes >> 4), idesc_pv,
-                        (j > 0 || kk > 0) ? 1u : 0u);
+                        (j > j0 || kk > 0) ? 1u : 0u);
           } else {
             for (int kk = 0; kk < nv / 16; ++kk)
               tc_mma_ts(o_tmem, pa + kk * 8, vd + (uint64_t)(kk * 16 * kRowBytes >> 4), idesc_pv,
-                        (j > 0 || kk > 0) ? 1u : 0u);
+                        (j > j0 || kk > 0) ? 1u : 0u);
           }
           tc_commit(smem_u32(&bars->pv_done[m]));
           tc_commit(smem_u32(&bars->kv_empty[ev]));
         }
         __syncwarp();
-        if (j + NBUF < n) {
-          // S of tile j + NBUF into buffer b, after P V(j) has read P(j) from it (in issue order)
-          ok = kv_wait(tb + j + NBUF, 0);
+        const int jn = j + NBUF * kStep;
+        if (jn < n) {
+          // S of the tile NBUF on into buffer b, after P V(j) has read P(j) from it (in issue order)
+          ok = kv_wait(tb + jn, 0);
           if (!ok) break;
           tc_fence_after();
-          issue_s(b, (tb + j + NBUF) % H, round16(tile_keys(p, x, sg.lo + j + NBUF).count));
+          issue_s(b, (tb + jn) % H, round16(tile_keys(p, x, sg.lo + jn).count));
         }
       }
       if (!ok) break;
@@ -672,15 +693,18 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
     mbar_wait(smem_u32(&bars->drain), 0, dw);
     __syncwarp();
   } else if (MX && warp >= 12 && have_work) {
-    if constexpr (MX) convert_tiles<D, NK>(p, sh, bars, smem, wc, c, warp - 12, lane);
+    if constexpr (MX) convert_tiles<D, NK, SPLIT>(p, sh, bars, smem, wc, c, warp - 12, lane);
   } else if (warp >= 4 && have_work) {
     // ========================================================= softmax WGs ==
     if constexpr (C::kSplitRegs) regs_inc<C::kSoftmaxRegs>();
     const int m = (warp - 4) >> 2;
     const int q4 = warp & 3;             // TMEM lane quarter of this warp
     const int row = q4 * 32 + lane;      // row within the M-tile
-    const int r = m * 128 + row;         // packed row of the unit
-    if (m < MT) {
+    const int mr = SPLIT ? 0 : m;        // M-tile of the rows
+    const int r = mr * 128 + row;        // packed row of the unit
+    const bool rows_here = mr * 128 + q4 * 32 < p.R;   // a warp without rows only keeps the barriers going
+    constexpr int kStep = SPLIT ? 2 : 1;
+    if (m < NS) {
       const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
       const uint32_t s_base = tmem + lane_off + m * 128;  // + buffer * NK
       const uint32_t o_addr = tmem + lane_off + 256 + m * D;
@@ -747,7 +771,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           else l += tile_exp_store<NK, kFull>(v, count, p.scale_log2, m_ref, s_addr);
           return true;
         };
-        for (int i = sg.lo; i < sg.hi; ++i, ++G) {
+        const int i0 = sg.lo + (SPLIT ? m : 0);
+        for (int i = i0; i < sg.hi; i += kStep, ++G) {
           const TileKeys tk = tile_keys(p, x, i);
           const int count = tk.count;
           unsigned long long mask = 0ull;
@@ -770,11 +795,13 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           tc_fence_after();
           // (128-key tiles keep a single masked path: a second copy of their 128-register body
           // would not fit the register budget)
-          if constexpr (NK == 128)
-            ok = tile(std::false_type{}, count, mask, s_addr, i == sg.lo);
+          if (!rows_here)
+            ok = true;
+          else if constexpr (NK == 128)
+            ok = tile(std::false_type{}, count, mask, s_addr, i == i0);
           else
-            ok = full ? tile(std::true_type{}, count, mask, s_addr, i == sg.lo)
-                      : tile(std::false_type{}, count, mask, s_addr, i == sg.lo);
+            ok = full ? tile(std::true_type{}, count, mask, s_addr, i == i0)
+                      : tile(std::false_type{}, count, mask, s_addr, i == i0);
           if (!ok) break;
           tc_wait_st();
           tc_fence_before();
@@ -782,12 +809,30 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
         }
         if (!ok) break;
         // ---- epilogue: O / l to the output (or the segment's partial) ----
+        float wa = 1.f, wb = 0.f;             // weights of the accumulators (SPLIT: of both)
+        bool has[2] = {true, false};
+        if constexpr (SPLIT) {
+          float2* ml = reinterpret_cast<float2*>(smem + C::kMlOff) + (seg_cnt & 1) * 256;
+          ml[m * 128 + row] = make_float2(m_ref, l);
+          mbar_arrive(smem_u32(&bars->ml_full));
+          ok = mbar_wait(smem_u32(&bars->ml_full), seg_cnt & 1, wc);
+          if (ok) ok = mbar_wait(smem_u32(&bars->o_full[m ^ 1]), seg_cnt & 1, wc);
+          if (!ok) break;
+          has[1] = sg.hi - sg.lo > 1;
+          const float2 a = ml[row], b = has[1] ? ml[128 + row] : make_float2(a.x, 0.f);
+          m_ref = fmaxf(a.x, b.x);
+          wa = fast_exp2(a.x - m_ref);
+          wb = has[1] ? fast_exp2(b.x - m_ref) : 0.f;
+          l = wa * a.y + wb * b.y;
+        }
         ok = mbar_wait(smem_u32(&bars->o_full[m]), seg_cnt & 1, wc);
         if (!ok) break;
         tc_fence_after();
         const bool none = VIS && (absent || l == 0.f);   // no visible key: 0, lse = -inf
         const float inv = none ? 0.f : 1.f / l;
-        const int rbase = m * 128 + q4 * 32;  // first packed row of this warp
+        wa *= inv;
+        wb *= inv;
+        const int rbase = mr * 128 + q4 * 32;  // first packed row of this warp
         // element offsets of the rows that this lane stores of a final output (every fourth) from the
         // unit's first row
         const size_t at0 = ((size_t)x.ns * p.S * p.Hq + x.h * p.g) * D + (lane & 7) * 4;
@@ -799,22 +844,39 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           at[k] = (t * p.Hq + (gr - t * p.g)) * D;
         }
         float* part = p.part_o + part_at(p, sg.slot, r, 0, D);   // four columns on: 4 R floats further
+        constexpr int kChunks = D / 32 / kStep;   // SPLIT: this warpgroup's half of the columns
+        const int c_lo = SPLIT ? m * kChunks : 0;
 #pragma unroll 1   // (cold code: fetched once, not four times)
-        for (int cc = 0; cc < D / 32; ++cc) {
+        for (int cc = c_lo; cc < c_lo + kChunks; ++cc) {
           uint32_t o[32];
-          tmem_ld32(o_addr + cc * 32, o);
-          tc_wait_ld();
-          if (cc == D / 32 - 1) {
+          if constexpr (SPLIT) {
+            uint32_t ob[32];
+            tmem_ld32(tmem + lane_off + 256 + cc * 32, o);
+            tmem_ld32(tmem + lane_off + 256 + D + cc * 32, ob);
+            tc_wait_ld();
+            // (an accumulator that took no P V holds anything: select, never scale by 0)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              o[k] = __float_as_uint(wa * __uint_as_float(o[k]) + (has[1] ? wb * __uint_as_float(ob[k]) : 0.f));
+          } else {
+            tmem_ld32(o_addr + cc * 32, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(wa * __uint_as_float(o[k]));
+          }
+          if (cc == c_lo + kChunks - 1) {
+            // O fully read: the next segment may overwrite it
             tc_fence_before();
-            mbar_arrive(smem_u32(&bars->o_empty[m]));  // O fully read: the next segment may overwrite it
+            mbar_arrive(smem_u32(&bars->o_empty[m]));
+            if constexpr (SPLIT) mbar_arrive(smem_u32(&bars->o_empty[m ^ 1]));
           }
           if (VIS && none) {   // (an absent row's query may be anything: its accumulator too)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
           auto four = [&](int q) {
-            return make_float4(__uint_as_float(o[4 * q]) * inv, __uint_as_float(o[4 * q + 1]) * inv,
-                               __uint_as_float(o[4 * q + 2]) * inv, __uint_as_float(o[4 * q + 3]) * inv);
+            return make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
+                               __uint_as_float(o[4 * q + 3]));
           };
           if (!sg.full) {
             if (r < p.R) {
@@ -837,7 +899,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (r < p.R) {
+        if (r < p.R && (!SPLIT || m == 0)) {
           const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * 0.6931471805599453f;
           if (sg.full) {
             if (p.lse) {
@@ -876,62 +938,76 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX>::kThreads, 1)
                                *(volatile int*)&sh->abort_flag != 0);
 }
 
-template <int D, int NK, bool VIS = false, bool MX = false>
-void set_smem_attr() {
-  cudaFuncSetAttribute(attn_tcgen05_kernel<D, NK, VIS, MX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                       Cfg<D, NK, MX>::kSmemBytes);
+// The opt-in shared-memory size (first asked for by the plan: not during a graph capture).
+template <int D, int NK, bool VIS, bool MX, bool SPLIT>
+cudaError_t prepare_as() {
+  static std::atomic<unsigned long long> done{0};
+  return smem_opt_in(reinterpret_cast<const void*>(&attn_tcgen05_kernel<D, NK, VIS, MX, SPLIT>),
+                     Cfg<D, NK, MX, SPLIT>::kSmemBytes, done);
+}
+template <int D, bool SPLIT>
+cudaError_t prepare64() {
+  cudaError_t e = prepare_as<D, 64, false, false, SPLIT>();
+  if (e == cudaSuccess) e = prepare_as<D, 64, true, false, SPLIT>();
+  if (e == cudaSuccess) e = prepare_as<D, 64, true, true, SPLIT>();
+  return e;
+}
+template <int D>
+cudaError_t prepare(int R) {
+  const cudaError_t e = R <= 128 ? prepare64<D, true>() : prepare64<D, false>();
+  return e != cudaSuccess ? e : prepare_as<D, 128, false, false, false>();
 }
 
-template <int D, int NK, bool VIS = false, bool MX = false>
-cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
+template <int D, int NK, bool VIS, bool MX, bool SPLIT>
+cudaError_t launch_as(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
+  using C = Cfg<D, NK, MX, SPLIT>;
+  const cudaError_t e = prepare_as<D, NK, VIS, MX, SPLIT>();
+  if (e != cudaSuccess) return e;
   // a programmatic dependent of the previous kernel on the stream (its setup overlaps that
   // kernel's tail), and cooperative when the fused combine needs every CTA resident at once
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.C, 1, 1);
-  cfg.blockDim = dim3(Cfg<D, NK, MX>::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<D, NK, MX>::kSmemBytes;
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeCooperative;
-  attr[1].val.cooperative = 1;
-  cfg.attrs = attr;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeCooperative;
+  attrs[1].val.cooperative = 1;
+  cfg.attrs = attrs;
   cfg.numAttrs = p.arrivals != nullptr ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK, VIS, MX>, p, maps);
+  return cudaLaunchKernelEx(&cfg, attn_tcgen05_kernel<D, NK, VIS, MX, SPLIT>, p, maps);
+}
+
+// Units of at most 128 rows: the two softmax warpgroups share the tiles (64-key tiles only).
+template <int D, bool VIS, bool MX>
+cudaError_t launch64(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
+  return p.R <= 128 ? launch_as<D, 64, VIS, MX, true>(p, maps, stream) : launch_as<D, 64, VIS, MX, false>(p, maps, stream);
+}
+template <int D>
+cudaError_t launch(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
+  // trees, quantised contexts, and paged windows whose first load may start before the window: 64-key tiles
+  const bool vis = p.parents || (p.window > 0 && p.win_align > 1);
+  if (p.key_tile == 128) {
+    if (vis || p.k_scale) return cudaErrorInvalidValue;
+    return launch_as<D, 128, false, false, false>(p, maps, stream);
+  }
+  if (p.k_scale) return launch64<D, true, true>(p, maps, stream);
+  return vis ? launch64<D, true, false>(p, maps, stream) : launch64<D, false, false>(p, maps, stream);
 }
 
 }  // namespace
 
+cudaError_t prepare_attn_tcgen05(int D, int R) { return D == 128 ? prepare<128>(R) : prepare<64>(R); }
+
 bool tcgen05_key_tile_supported(int key_tile) { return key_tile == 64 || key_tile == 128; }
 
 cudaError_t launch_attn_tcgen05(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
-  static const bool attr_done = [] {
-    set_smem_attr<128, 128>();
-    set_smem_attr<128, 64>();
-    set_smem_attr<64, 128>();
-    set_smem_attr<64, 64>();
-    set_smem_attr<128, 64, true>();
-    set_smem_attr<64, 64, true>();
-    set_smem_attr<128, 64, true, true>();
-    set_smem_attr<64, 64, true, true>();
-    return true;
-  }();
-  (void)attr_done;
   if (!tcgen05_key_tile_supported(p.key_tile)) return cudaErrorInvalidValue;
-  if (p.k_scale) {   // quantised context
-    if (p.key_tile != 64) return cudaErrorInvalidValue;
-    return p.D == 128 ? launch<128, 64, true, true>(p, maps, stream) : launch<64, 64, true, true>(p, maps, stream);
-  }
-  // trees, and paged windows whose first load may start before the window: 64-key tiles
-  if (p.parents || (p.window > 0 && p.win_align > 1)) {
-    if (p.key_tile != 64) return cudaErrorInvalidValue;
-    return p.D == 128 ? launch<128, 64, true>(p, maps, stream) : launch<64, 64, true>(p, maps, stream);
-  }
   // variant 2: head_dim 128 with 128-key tiles on the transposed-PV kernel (attn_tcgen05_pt.cu)
   if (p.D == 128 && p.key_tile == 128 && p.variant == 2) return launch_attn_pt(p, maps, stream);
-  if (p.D == 128) return p.key_tile == 128 ? launch<128, 128>(p, maps, stream) : launch<128, 64>(p, maps, stream);
-  return p.key_tile == 128 ? launch<64, 128>(p, maps, stream) : launch<64, 64>(p, maps, stream);
+  return p.D == 128 ? launch<128>(p, maps, stream) : launch<64>(p, maps, stream);
 }
 
 }  // namespace tt

@@ -42,6 +42,7 @@
 
 #include "problem.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "tc_common.cuh"
 #include "walker.cuh"
 
@@ -637,11 +638,9 @@ int attn_2sm_max_clusters() {
 }
 
 cudaError_t launch_attn_2sm(const Problem& p, cudaStream_t stream) {
-  static const bool attr_done = [] {
-    cudaFuncSetAttribute(attn_2sm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    return true;
-  }();
-  (void)attr_done;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t opt = smem_opt_in(reinterpret_cast<const void*>(&attn_2sm_kernel), kSmemBytes, done);
+  if (opt != cudaSuccess) return opt;
   if (!attn_2sm_supported(p.D, p.g) || p.key_tile != kNK) return cudaErrorInvalidValue;
   TmaMaps maps;
   memset(&maps, 0, sizeof(maps));

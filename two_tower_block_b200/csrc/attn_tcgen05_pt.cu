@@ -34,6 +34,7 @@
 // error word and returns.
 #include "problem.h"
 #include "ptx.cuh"
+#include "smem_opt_in.h"
 #include "tc_common.cuh"
 #include "walker.cuh"
 
@@ -478,11 +479,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t attn_pt_smem_bytes() { return kSmemBytes; }
 
 cudaError_t launch_attn_pt(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
-  static const bool attr_done = [] {
-    cudaFuncSetAttribute(attn_pt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    return true;
-  }();
-  (void)attr_done;
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t opt = smem_opt_in(reinterpret_cast<const void*>(&attn_pt_kernel), kSmemBytes, done);
+  if (opt != cudaSuccess) return opt;
   if (p.D != kD) return cudaErrorInvalidValue;
   attn_pt_kernel<<<p.C, kThreads, kSmemBytes, stream>>>(p, maps);
   return cudaGetLastError();

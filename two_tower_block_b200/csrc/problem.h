@@ -88,6 +88,7 @@ struct TmaMaps {
   CUtensorMap q, k_ctx, v_ctx, k_blk, v_blk;
 };
 cudaError_t launch_attn_tcgen05(const Problem& p, const TmaMaps& maps, cudaStream_t stream);
+cudaError_t prepare_attn_tcgen05(int D, int R);   // of the current device, before the first launch
 bool tcgen05_key_tile_supported(int key_tile);
 cudaError_t launch_attn_pt(const Problem& p, const TmaMaps& maps, cudaStream_t stream);
 // 2-SM kernel (cluster of two CTAs, one range per cluster): head_dim 128, 128 % g == 0
