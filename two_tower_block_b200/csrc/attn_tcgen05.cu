@@ -271,11 +271,8 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
   constexpr int H = C::kStages / 2, kRowScale = D / kMxBlock;
   const int kv = w >> 1, first_row = 32 * (w & 1);
   const long long start = sh->start, end = sh->end;
-  // lane's chunks of a tile: the k4-th 16 bytes of one half of row_of(e)
-  constexpr int kChunks = 4 * C::kHalves;
-  const int k4 = lane & 3;
-  auto row_of = [&](int e) { return e / C::kHalves * 8 + (lane >> 2); };
-  auto half_of = [&](int e) { return C::kHalves == 2 ? (e ^ (lane >> 2)) & 1 : 0; };
+  // lane's 16-byte chunk of a row's half: the k4-th, of row r0 + lane / 4
+  const int k4 = lane & 3, r4 = lane >> 2;
   uint32_t k = 0, t = 0;   // raw tiles converted, tiles of the CTA passed
   bool ok = true;
   Unit x = sh->first;
@@ -284,30 +281,6 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
     for (int i = sg.lo; i < sg.hi; ++i, ++t) {
       const uint32_t stage = kv * H + t % H;
       const bool blk = i < p.blk_tiles;
-      uint4 b[kChunks];
-      uint32_t byte[kChunks];
-      uint32_t mask = 0;
-      int n = 0;
-      if (!blk) {
-        const uint32_t slot = k % C::kRaw;
-        ok = mbar_wait_warp(smem_u32(&bars->raw_full[slot]), (k / C::kRaw) & 1, wc);
-        if (!ok) break;
-        const uint8_t* in = smem + C::kRawOff + slot * C::kRawBytes;
-        const TileKeys tk = tile_keys(p, x, i);
-        n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
-        const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
-        mask = *reinterpret_cast<const uint32_t*>(in + C::kRawMask + first_row / 8);
-        const uint8_t* sc = in + C::kRawScale + kv * C::kScaleBytes + (first_row + odd) * kRowScale;
-        in += (kv * NK + first_row) * D;
-#pragma unroll
-        for (int e = 0; e < kChunks; ++e) {
-          b[e] = *reinterpret_cast<const uint4*>(in + row_of(e) * D + half_of(e) * 64 + k4 * 16);
-          byte[e] = sc[row_of(e) * kRowScale + half_of(e) * 2 + (k4 >> 1)];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[slot]));
-        ++k;
-      }
       // every tile's free slot is waited for here, in order (a barrier's parity tells only one
       // use from the next); a block tile's is handed on to its producer warp, by both converter
       // warps and on a barrier of that slot, so that no barrier runs ahead of one who waits on it
@@ -318,34 +291,68 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
         if (lane == 0 && t >= (uint32_t)H) mbar_arrive(smem_u32(&bars->blk_go[stage]));
         continue;
       }
-      uint8_t* tile = smem + C::kStageOff + stage * C::kSlotBytes + first_row * kRowBytes;
-      auto store = [&](int e, uint4 lo, uint4 hi) {
-        uint8_t* to = tile + half_of(e) * (NK * kRowBytes) + row_of(e) * kRowBytes;
-        *reinterpret_cast<uint4*>(to + (((2 * k4) ^ (row_of(e) & 7)) << 4)) = lo;
-        *reinterpret_cast<uint4*>(to + (((2 * k4 + 1) ^ (row_of(e) & 7)) << 4)) = hi;
+      const uint32_t slot = k % C::kRaw;
+      ok = mbar_wait_warp(smem_u32(&bars->raw_full[slot]), (k / C::kRaw) & 1, wc);
+      if (!ok) break;
+      const uint8_t* raw = smem + C::kRawOff + slot * C::kRawBytes;
+      const TileKeys tk = tile_keys(p, x, i);
+      const int n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
+      const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
+      const uint32_t mask = *reinterpret_cast<const uint32_t*>(raw + C::kRawMask + first_row / 8);
+      const uint8_t* in = raw + (kv * NK + first_row + r4) * D + k4 * 16;
+      const uint8_t* sc = raw + C::kRawScale + kv * C::kScaleBytes + (first_row + r4 + odd) * kRowScale + (k4 >> 1);
+      uint8_t* to = smem + C::kStageOff + stage * C::kSlotBytes + (first_row + r4) * kRowBytes;
+      // The conversion is bound by the integer pipe (three operations a pair), so the full rows of most
+      // pieces run without selects, and 16 rows at a time with constant offsets from the two halves
+      // of a row in lane's order (one half of head_dim 64).  Not longer: the warps of an SM
+      // sub-partition run different code, and what is unrolled further is waited for as
+      // instruction fetches (a batch of drafted trees: 241 us rolled, 280 with 32 rows at a time).
+      const int h0 = C::kHalves == 2 ? r4 & 1 : 0;
+      auto chunk_in = [&](int h, int r0) { return in + (h0 ^ h) * 64 + r0 * D; };
+      auto chunk_sc = [&](int h, int r0) { return sc + (h0 ^ h) * 2 + r0 * kRowScale; };
+      auto chunk_to = [&](int h, int r0, int c2) {
+        return reinterpret_cast<uint4*>(to + (h0 ^ h) * (NK * kRowBytes) + (((2 * k4 + c2) ^ r4) << 4) + r0 * kRowBytes);
       };
-      uint32_t top = 0;
-#pragma unroll
-      for (int e = 0; e < kChunks; ++e) top = max(top, byte[e]);
-      if (__all_sync(0xffffffffu, mask == 0xffffffffu && top <= kMxOneFactor)) {
+#pragma unroll 1
+      for (int rr = 0; rr < n; rr += 16) {
+        constexpr int kChunks = 2 * C::kHalves;   // of lane: rows rr + r4 and rr + 8 + r4
+        uint4 b[kChunks];
+        uint32_t byte[kChunks], top = 0;
 #pragma unroll
         for (int e = 0; e < kChunks; ++e) {
-          const uint32_t f = mx_factor(byte[e]);
-          const uint2 b0 = mx_to_bf16x4(b[e].x, f), b1 = mx_to_bf16x4(b[e].y, f);
-          const uint2 b2 = mx_to_bf16x4(b[e].z, f), b3 = mx_to_bf16x4(b[e].w, f);
-          store(e, make_uint4(b0.x, b0.y, b1.x, b1.y), make_uint4(b2.x, b2.y, b3.x, b3.y));
+          b[e] = *reinterpret_cast<const uint4*>(chunk_in(e % C::kHalves, rr + e / C::kHalves * 8));
+          byte[e] = *chunk_sc(e % C::kHalves, rr + e / C::kHalves * 8);
+          top = max(top, byte[e]);
         }
-      } else {
+        if (__all_sync(0xffffffffu, ((mask >> rr) & 0xffffu) == 0xffffu && top <= kMxOneFactor)) {
 #pragma unroll
-        for (int e = 0; e < kChunks; ++e) {
-          if (row_of(e) >= n) continue;
-          if (!((mask >> row_of(e)) & 1u)) b[e] = make_uint4(0, 0, 0, 0);
-          store(e, mx_to_bf16x8(make_uint2(b[e].x, b[e].y), byte[e]), mx_to_bf16x8(make_uint2(b[e].z, b[e].w), byte[e]));
+          for (int e = 0; e < kChunks; ++e) {
+            const int h = e % C::kHalves, r0 = rr + e / C::kHalves * 8;
+            const uint32_t f = (byte[e] + 120u) * 0x00800080u;   // mx_factor of a byte up to kMxOneFactor
+            const uint2 b0 = mx_to_bf16x4(b[e].x, f), b1 = mx_to_bf16x4(b[e].y, f);
+            const uint2 b2 = mx_to_bf16x4(b[e].z, f), b3 = mx_to_bf16x4(b[e].w, f);
+            *chunk_to(h, r0, 0) = make_uint4(b0.x, b0.y, b1.x, b1.y);
+            *chunk_to(h, r0, 1) = make_uint4(b2.x, b2.y, b3.x, b3.y);
+          }
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < kChunks; ++e) {
+            const int h = e % C::kHalves, r0 = rr + e / C::kHalves * 8;
+            uint4 v = *reinterpret_cast<const uint4*>(chunk_in(h, r0));
+            const uint32_t vb = *chunk_sc(h, r0);
+            if (!((mask >> (r0 + r4)) & 1u)) v = make_uint4(0, 0, 0, 0);
+            *chunk_to(h, r0, 0) = mx_to_bf16x8(make_uint2(v.x, v.y), vb);
+            *chunk_to(h, r0, 1) = mx_to_bf16x8(make_uint2(v.z, v.w), vb);
+          }
         }
       }
+      ++k;
       fence_proxy_async_smem();
-      __syncwarp();   // every lane has written its share of the tile
-      if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[stage]));
+      __syncwarp();   // every lane has read its raw bytes and written its share of the tile
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&bars->kv_full[stage]));
+        mbar_arrive(smem_u32(&bars->raw_empty[slot]));
+      }
     }
     if (!ok || sg.last) break;
     x = next_unit(p, x);

@@ -138,6 +138,20 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same, suspending the thread for up to `ns` while the phase is incomplete.
+__device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
+// Waiting warps suspend rather than poll: polling ones take issue slots from the working ones of
+// their SM sub-partition.
+constexpr uint32_t kSuspendNs = 20000;
+
 // Context of a bounded wait: a CTA-wide abort flag in shared memory, the
 // global error word, and the limit of a single wait.
 struct WaitCtx {
@@ -153,7 +167,7 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
   if (mbar_try_wait(bar, parity)) return true;
   const unsigned long long t0 = timer_start();
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
     if ((it & 15u) == 0u) {
       if (*w.abort_flag) return false;
       if (timer_over(t0, w.limit_ns)) {

@@ -494,11 +494,24 @@ class Plan:
     def block_attn_block_causal(self, q, k_ctx, v_ctx, k_blk, v_blk, out=None, lse=None, stream=None,
                                 want_lse=False):
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.seq_len)
-        q_, kc, vc, kb, vb, o, l = _addrs(self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse,
-                                                                          self._out_kind()))
+        want = self._usual_causal
+        x = (q, k_ctx, v_ctx, k_blk, v_blk, out)
+        at = _quick(self.device, x if lse is None else x + (lse,), want[0] + ((self.out_dtype, want[0][0][1]), want[1]))
+        if at is not None and lse is None:
+            at.append(None)
+        q_, kc, vc, kb, vb, o, l = at or _addrs(
+            self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse, self._out_kind()))
         _check(lib().tt_block_attn_block_causal(self._h, q_, kc, vc, kb, vb, o, l, self._on(stream)),
                "tt_block_attn_block_causal")
         return (out, lse) if lse is not None else out
+
+    @functools.cached_property
+    def _usual_causal(self):
+        """What _quick wants of q, k_ctx, v_ctx, k_blk and v_blk of a block-causal call, and of its lse."""
+        s = self.shape
+        n, b = s.batch * s.seq_len, torch.bfloat16
+        k = (b, n * s.kv_heads * s.head_dim)
+        return ((b, n * s.q_heads * s.head_dim), k, k, k, k), (torch.float32, n * s.q_heads)
 
     def _causal_items(self, q, k_ctx, v_ctx, k_blk, v_blk, out, lse, out_kind="f32"):
         s = self.shape
@@ -522,7 +535,10 @@ class Plan:
             dv_blk = torch.empty_like(dk_blk)
         nq = s.batch * s.seq_len * s.q_heads * s.head_dim
         nk = s.batch * s.seq_len * s.kv_heads * s.head_dim
-        q_, kc, vc, kb, vb, o, l, do, dq_, dk, dv = _addrs(
+        want, f = self._usual_causal, torch.float32
+        at = _quick(self.device, (q, k_ctx, v_ctx, k_blk, v_blk, out, lse, dout, dq, dk_blk, dv_blk),
+                    want[0] + ((f, nq), want[1], (torch.bfloat16, nq), (f, nq), (f, nk), (f, nk)))
+        q_, kc, vc, kb, vb, o, l, do, dq_, dk, dv = at or _addrs(
             self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse)
             + ((dout, "dout", nq, "bf16"), (dq, "dq", nq, "f32"), (dk_blk, "dk_blk", nk, "f32"),
                (dv_blk, "dv_blk", nk, "f32")))
@@ -536,8 +552,11 @@ class Plan:
         place; advance ctx_lens (device int32) by S when `advance`."""
         s = self.shape
         nb = s.batch * s.block * s.kv_heads * s.head_dim
-        kn, vn, kc, vc, lens = _addrs(self.device, ((k_new, "k_new", nb, "bf16"), (v_new, "v_new", nb, "bf16"))
-                                      + self._slab_items(k_ctx, v_ctx) + ((ctx_lens, "ctx_lens", s.batch, "i32"),))
+        usual = self._usual
+        at = _quick(self.device, (k_new, v_new, k_ctx, v_ctx, ctx_lens), usual[0][1:3] + usual[1] + usual[0][3:4])
+        kn, vn, kc, vc, lens = at or _addrs(
+            self.device, ((k_new, "k_new", nb, "bf16"), (v_new, "v_new", nb, "bf16"))
+            + self._slab_items(k_ctx, v_ctx) + ((ctx_lens, "ctx_lens", s.batch, "i32"),))
         _check(lib().tt_kv_append(self._h, kn, vn, kc, vc, lens, int(bool(advance)), self._on(stream)),
                "tt_kv_append")
 
