@@ -2,7 +2,8 @@
 
 Usage: python -m two_tower_block_b200.build [--force] [-v]
 Objects go to two_tower_block_b200/_build/; the shared library is written
-next to this file so that it travels with the source tree.
+next to this file so that it travels with the source tree, and so is _marshal.so,
+the argument marshalling of the Python binding (the only part that knows torch).
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +20,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtt_block_attn.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -30,6 +33,16 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
+def _marshal_cmd(src):
+    import torch
+    t = os.path.dirname(torch.__file__)
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(t, "include"),
+            "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
+            "-I" + sysconfig.get_paths()["include"], src, "-o", MARSHAL + ".tmp", "-L" + os.path.join(t, "lib"),
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+
+
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
@@ -38,6 +51,8 @@ def _headers():
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
+    binding = os.path.join(CSRC, "marshal.cpp")
+    srcs.remove(binding)
     hdr_mtime = max((os.path.getmtime(h) for h in _headers()), default=0.0)
     jobs = []
     objs = []
@@ -48,6 +63,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             cmd = [nvcc()] + ARCH + FLAGS + (["-Xptxas", "-v"] if ptxas_info and s.endswith(".cu") else [])
             cmd += ["-x", "cu" if s.endswith(".cu") else "c++", "-c", s, "-o", o]
             jobs.append(cmd)
+
+    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(binding):
+        jobs.append(_marshal_cmd(binding))
 
     def run(cmd):
         if verbose:
@@ -60,7 +78,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             if r.returncode != 0 or verbose or ptxas_info:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
+                raise RuntimeError("build failed: " + " ".join(cmd))
+    if os.path.exists(MARSHAL + ".tmp"):
+        os.replace(MARSHAL + ".tmp", MARSHAL)
     if jobs or force or not os.path.exists(LIB):
         cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp"] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

@@ -168,10 +168,11 @@ _USUAL = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8"
           "e4m3": torch.float8_e4m3fn}
 
 
-def _quick(device, tensors, want):
-    """Addresses of tensors that are all of the usual type, the right size, contiguous and on the device:
-    one look at each, since a small call's host time is what it waits for.  ``want``: (dtype, numel) of
-    each.  None if one is not (or is no tensor): _addrs then says what is wrong, or takes it."""
+def _quick_py(device, tensors, want):
+    """Addresses of tensors that are all of the usual type, the right size, contiguous and on the device
+    (-1: the CPU): one look at each, since a small call's host time is what it waits for.  ``want``:
+    (dtype, numel) of each.  None if one is not (or is no tensor): _addrs then says what is wrong, or
+    takes it."""
     at = []
     try:
         for t, (dtype, numel) in zip(tensors, want):
@@ -181,6 +182,12 @@ def _quick(device, tensors, want):
     except AttributeError:
         return None
     return at
+
+
+try:   # the same in C++ (csrc/marshal.cpp), a tenth of the time; built beside the library
+    from ._marshal import addresses as _quick
+except ImportError:
+    _quick = _quick_py
 
 
 def _addrs(device, items):
@@ -217,24 +224,27 @@ class MxCache:
     `page_table` [B, pages_per_seq] pools [num_pages, Hkv, P, D].  Holds the tensors it describes."""
 
     def __init__(self, k, k_scale, v, v_scale, page_table=None):
-        if k.dim() != 4 or k.shape[3] % 32:
-            raise ValueError(f"k: shape {tuple(k.shape)}, expected four dimensions, the last a multiple of 32")
+        shape = k.shape
+        if len(shape) != 4 or shape[3] % 32:
+            raise ValueError(f"k: shape {tuple(shape)}, expected four dimensions, the last a multiple of 32")
         self.k, self.k_scale, self.v, self.v_scale, self.page_table = k, k_scale, v, v_scale, page_table
-        self.shape = tuple(k.shape)
+        self.shape = shape
+        self._device = k.get_device() if k.is_cuda else -1
         n = k.numel()
-        items = [(k, "k", n, "e4m3"), (v, "v", n, "e4m3"), (k_scale, "k_scale", n // 32, "u8"),
-                 (v_scale, "v_scale", n // 32, "u8")]
-        num_pages = page_size = pages_per_seq = 0
+        values, scales = (torch.float8_e4m3fn, n), (torch.uint8, n // 32)
+        tensors, want = (k, v, k_scale, v_scale), (values, values, scales, scales)
+        num_pages = page_size = pages_per_seq = table = 0
         if page_table is not None:
             if page_table.dim() != 2:
                 raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [B, pages_per_seq]")
-            num_pages, page_size, pages_per_seq = k.shape[0], k.shape[2], page_table.shape[1]
-            items.append((page_table, "page_table", page_table.numel(), "i32"))
-        self.device = k.device
-        # (a device cache's tensors are all on that device; a host one is refused by the calls)
-        dev = k.get_device() if k.is_cuda else None
-        at = _quick(dev, [t for t, _, _, _ in items], [(_USUAL[kind], m) for _, _, m, kind in items]) or \
-            _addrs(dev, items)
+            num_pages, page_size, pages_per_seq, table = shape[0], shape[2], page_table.shape[1], page_table.numel()
+            tensors, want = tensors + (page_table,), want + ((torch.int32, table),)
+        at = _quick(self._device, tensors, want)
+        if at is None:
+            # (a device cache's tensors are all on that device; a host one is refused by the calls)
+            items = [(k, "k", n, "e4m3"), (v, "v", n, "e4m3"), (k_scale, "k_scale", n // 32, "u8"),
+                     (v_scale, "v_scale", n // 32, "u8"), (page_table, "page_table", table, "i32")]
+            at = _addrs(self._device if self._device >= 0 else None, items)
         self._d = MxCacheDesc(at[0], at[1], at[2], at[3], at[4] if page_table is not None else None, num_pages,
                               page_size, pages_per_seq)
         self._ref = ctypes.byref(self._d)
@@ -251,14 +261,15 @@ class MxCache:
     def _fits(self, plan):
         """The cache's layout against a plan's shape and device."""
         s = plan.shape
-        if self.device.type != "cuda" or self.device.index != plan.device:
-            raise ValueError(f"cache: expected on cuda:{plan.device}, got {self.device}")
+        shape = self.shape
+        if self._device != plan.device:
+            raise ValueError(f"cache: expected on cuda:{plan.device}, got {self.k.device}")
         if self.page_table is None:
             want = (s.batch, s.kv_heads, s.ctx_capacity, s.head_dim)
-            if self.shape != want:
-                raise ValueError(f"cache: shape {self.shape}, expected {want}")
-        elif self.shape[1] != s.kv_heads or self.shape[3] != s.head_dim or self.page_table.shape[0] != s.batch:
-            raise ValueError(f"cache: pages {self.shape} with a table {tuple(self.page_table.shape)}, expected "
+            if shape != want:
+                raise ValueError(f"cache: shape {tuple(shape)}, expected {want}")
+        elif shape[1] != s.kv_heads or shape[3] != s.head_dim or self.page_table.shape[0] != s.batch:
+            raise ValueError(f"cache: pages {tuple(shape)} with a table {tuple(self.page_table.shape)}, expected "
                              f"[num_pages, {s.kv_heads}, P, {s.head_dim}] and [{s.batch}, pages_per_seq]")
         return self._ref
 
@@ -360,17 +371,19 @@ class Plan:
         if k_pages is None:
             num_pages, page_size = 0, 16      # no pool: valid only without context (the library checks)
         else:
-            if k_pages.dim() != 4 or k_pages.shape[1] != s.kv_heads or k_pages.shape[3] != s.head_dim:
+            shape = k_pages.shape
+            if len(shape) != 4 or shape[1] != s.kv_heads or shape[3] != s.head_dim:
                 raise ValueError(f"k_pages: shape {tuple(k_pages.shape)}, expected [num_pages, {s.kv_heads}, P, "
                                  f"{s.head_dim}]")
-            num_pages, _, page_size, _ = k_pages.shape
+            num_pages, page_size = shape[0], shape[2]
         pool_numel = k_pages.numel() if k_pages is not None else 0
         pages_per_seq = 0
         if page_table is not None:
-            if page_table.dim() != 2 or page_table.shape[0] != s.batch:
-                raise ValueError(f"page_table: shape {tuple(page_table.shape)}, expected [{s.batch}, pages_per_seq]")
-            pages_per_seq = page_table.shape[1]
-        return int(num_pages), int(page_size), int(pages_per_seq), lambda: (
+            shape = page_table.shape
+            if len(shape) != 2 or shape[0] != s.batch:
+                raise ValueError(f"page_table: shape {tuple(shape)}, expected [{s.batch}, pages_per_seq]")
+            pages_per_seq = shape[1]
+        return num_pages, page_size, pages_per_seq, lambda: (
             (k_pages, "k_pages", pool_numel, "bf16"), (v_pages, "v_pages", pool_numel, "bf16"),
             (page_table, "page_table", s.batch * pages_per_seq, "i32")), (
             (torch.bfloat16, pool_numel), (torch.bfloat16, pool_numel), (torch.int32, s.batch * pages_per_seq))
@@ -461,24 +474,26 @@ class Plan:
         """Quantise k_new/v_new [B, rows, Hkv, D] into the cache at [L_n, L_n + counts[n]) (all rows
         without ``counts``) and advance ctx_lens (device int32) when ``advance``."""
         s = self.shape
-        if k_new.dim() != 4 or k_new.shape[0] != s.batch or k_new.shape[2:] != (s.kv_heads, s.head_dim):
+        shape = k_new.shape
+        if len(shape) != 4 or shape[0] != s.batch or shape[2] != s.kv_heads or shape[3] != s.head_dim:
             raise ValueError(f"k_new: shape {tuple(k_new.shape)}, expected [{s.batch}, rows, {s.kv_heads}, "
                              f"{s.head_dim}]")
         n = k_new.numel()
         kn, vn, lens, cnt = self._rows_args(k_new, v_new, n, ctx_lens, counts, ("k_new", "v_new", "counts"))
-        _check(lib().tt_kv_append_mx(self._h, kn, vn, k_new.shape[1], cnt, cache._fits(self), lens,
+        _check(lib().tt_kv_append_mx(self._h, kn, vn, shape[1], cnt, cache._fits(self), lens,
                                      int(bool(advance)), self._on(stream)), "tt_kv_append_mx")
 
     def kv_read_mx(self, cache, ctx_lens, starts, k_out, v_out, stream=None):
         """Positions [starts[n], starts[n] + rows) below ctx_lens[n] back as bf16 into k_out/v_out
         [B, Hkv, rows, D] (``starts`` None: 0); other rows are left as they were."""
         s = self.shape
-        if k_out.dim() != 4 or k_out.shape[:2] != (s.batch, s.kv_heads) or k_out.shape[3] != s.head_dim:
+        shape = k_out.shape
+        if len(shape) != 4 or shape[0] != s.batch or shape[1] != s.kv_heads or shape[3] != s.head_dim:
             raise ValueError(f"k_out: shape {tuple(k_out.shape)}, expected [{s.batch}, {s.kv_heads}, rows, "
                              f"{s.head_dim}]")
         n = k_out.numel()
         ko, vo, lens, st = self._rows_args(k_out, v_out, n, ctx_lens, starts, ("k_out", "v_out", "starts"))
-        _check(lib().tt_kv_read_mx(self._h, cache._fits(self), lens, st, k_out.shape[2], ko, vo, self._on(stream)),
+        _check(lib().tt_kv_read_mx(self._h, cache._fits(self), lens, st, shape[2], ko, vo, self._on(stream)),
                "tt_kv_read_mx")
         return k_out, v_out
 
@@ -495,10 +510,13 @@ class Plan:
                                 want_lse=False):
         out, lse = self._outputs(q, out, lse, want_lse, self.shape.seq_len)
         want = self._usual_causal
-        x = (q, k_ctx, v_ctx, k_blk, v_blk, out)
-        at = _quick(self.device, x if lse is None else x + (lse,), want[0] + ((self.out_dtype, want[0][0][1]), want[1]))
-        if at is not None and lse is None:
-            at.append(None)
+        x, w = (q, k_ctx, v_ctx, k_blk, v_blk, out), want[0] + ((self.out_dtype, want[0][0][1]),)
+        if lse is None:
+            at = _quick(self.device, x, w)
+            if at is not None:
+                at.append(None)
+        else:
+            at = _quick(self.device, x + (lse,), w + (want[1],))
         q_, kc, vc, kb, vb, o, l = at or _addrs(
             self.device, self._causal_items(q, k_ctx, v_ctx, k_blk, v_blk, out, lse, self._out_kind()))
         _check(lib().tt_block_attn_block_causal(self._h, q_, kc, vc, kb, vb, o, l, self._on(stream)),
