@@ -181,11 +181,13 @@ tt::Problem base_problem(tt_plan_t plan) {
   p.sinks = plan->sinks;
   p.win_align = 1;
   p.unit_cost = 0;
+  p.whole_tiles = 0;
   p.parents = nullptr;
   return p;
 }
 
-tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s) {
+// combine: false when no unit can be cut.
+tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s, bool combine = true) {
   cudaError_t e;
   prof_mark(plan, 0, s, true);
   if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 3) {
@@ -245,7 +247,7 @@ tt_status_t launch_all(tt_plan_t plan, const tt::Problem& p, cudaStream_t s) {
   }
   prof_mark(plan, 0, s, false);
   if (e != cudaSuccess) return cuda_fail(e, "attention kernel launch");
-  if (p.C > 1 && p.arrivals == nullptr) {
+  if (combine && p.C > 1 && p.arrivals == nullptr) {
     prof_mark(plan, 1, s, true);
     e = tt::launch_combine(p, s);
     prof_mark(plan, 1, s, false);
@@ -305,6 +307,18 @@ std::vector<long long> weighted_causal_starts(const std::vector<int>& pref, long
 }
 
 constexpr int kDecodeUnitCost = 5;   // key tiles
+constexpr int kWholeUnitTiles = 6;
+
+// Whether a range of its own for every unit is possible (num_ctas set by the caller: not wanted).
+bool whole_units_fit(const tt_block_attn_desc& d, const tt::Problem& p) {
+  return d.num_ctas <= 0 && (long long)p.B * p.Hkv * p.NB <= p.C;
+}
+// Tiles of a unit at most.
+long long most_unit_tiles(const tt::Problem& p) {
+  const long long most = p.blk_tiles + (long long)tt::ceil_div(p.ctx_stride, p.key_tile);
+  if (p.window <= 0) return most;
+  return std::min(most, p.blk_tiles + 4 + (long long)p.window / p.key_tile + p.sinks / p.key_tile);
+}
 
 // The context of a decode call: contiguous slabs, or pages; bf16, or e4m3 with scales.
 struct CtxCache {
@@ -366,6 +380,7 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
   p.mode = tt::kDecode;
   p.NB = 1;
   const bool mx = c.k_scale != nullptr;
+  bool combine = true;
   if (c.paged || parents || mx) {
     // these forms live in the default tcgen05 kernel (and the mma.sync one)
     p.variant = 0;
@@ -393,13 +408,21 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
   p.v_scale = c.v_scale;
   p.k_blk = static_cast<const __nv_bfloat16*>(k_blk);
   p.v_blk = static_cast<const __nv_bfloat16*>(v_blk);
-  // ragged batches: a unit costs about five tiles beyond its own (sched.cuh) on the default kernel
-  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 0) p.unit_cost = kDecodeUnitCost;
+  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 0) {
+    // ragged batches: a unit costs about five tiles beyond its own (sched.cuh) on the default kernel
+    p.unit_cost = kDecodeUnitCost;
+    // short contexts: a cut costs a partial and its combine, whole units only their own tiles
+    if (whole_units_fit(d, p)) p.whole_tiles = kWholeUnitTiles;
+    if (most_unit_tiles(p) <= p.whole_tiles) {   // no length can cut one: nothing to combine
+      p.arrivals = nullptr;
+      combine = false;
+    }
+  }
   p.ctx_lens = ctx_lens;
   p.parents = parents;
   p.out = out;
   p.lse = lse;
-  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream), combine);
 }
 
 // The rows of a quantised cache as the write and read-back kernels take them, checked.
@@ -603,7 +626,10 @@ tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int
       unit_tiles = d.ctx_capacity > 0 ? std::min(unit_tiles, w) : w;
     }
     // (a plan without a context capacity or window serves paged calls, whose lengths it cannot bound)
-    const bool short_ranges = decode_aligned && (d.ctx_capacity > 0 || window > 0) &&
+    // (nor for units of at most 128 rows, whose partials are small: 9.9 against 11.3 us for a small
+    // tree, 13.2 against 13.8 for 16 rows over a window, and a cooperative launch costs 2.5 us more
+    // outside of a graph)
+    const bool short_ranges = decode_aligned && P->R > 128 && (d.ctx_capacity > 0 || window > 0) &&
                               unit_tiles * d.batch * d.num_kv_heads <= 32LL * std::max(P->C_decode, 1);
     P->fused_decode = can && P->C_decode <= P->sm_count && (force == 1 || (force != 0 && short_ranges));
   }
@@ -804,7 +830,14 @@ tt_status_t tt_block_attn_block_causal(tt_plan_t plan, const void* q, const void
   p.T_causal = plan->causal_T;
   p.causal_pref = plan->causal_pref;
   p.causal_starts = plan->causal_starts;
-  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream));
+  bool combine = true;
+  if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 0 && whole_units_fit(d, p) &&
+      most_unit_tiles(p) <= kWholeUnitTiles) {
+    p.whole_tiles = kWholeUnitTiles;
+    p.arrivals = nullptr;
+    combine = false;
+  }
+  return launch_all(plan, p, reinterpret_cast<cudaStream_t>(stream), combine);
 }
 
 tt_status_t tt_block_attn_host(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx, const void* k_blk,

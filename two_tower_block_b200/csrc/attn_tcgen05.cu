@@ -522,19 +522,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         if constexpr (VIS) {
           if (kv == 1) {
             zero = span_mask(0, round16(tk.count)) & ~span_mask(tk.head, tk.count);
-            if (tk.is_blk && p.parents) {
-              short* up = reinterpret_cast<short*>(smem + C::kTreeOff);
-              if (i == sg.lo) tree_rows(p, x.n, 0, lane, up, nullptr);   // (a segment may begin past tile 0)
-#pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const int t = 32 * w + lane;
-                zero |= (unsigned long long)__ballot_sync(0xffffffffu, t < tk.count && up[tk.first + t] == kAbsent)
-                        << (32 * w);
-              }
-            }
           }
         }
-        const bool fix = VIS ? zero != 0ull : kv == 1 && (tk.count & 15) != 0;
+        const bool tree = VIS && kv == 1 && tk.is_blk && p.parents;   // which rows are absent: while the loads run
+        const bool fix = VIS ? tree || zero != 0ull : kv == 1 && (tk.count & 15) != 0;
         const uint32_t bar = fix ? smem_u32(&bars->tail) : smem_u32(&bars->kv_full[s]);
         if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
         if (nsl > 0) {
@@ -552,6 +543,16 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
           }
         }
         if (MX && lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));   // for the second converter warp
+        if (tree) {
+          short* up = reinterpret_cast<short*>(smem + C::kTreeOff);
+          if (i == sg.lo) tree_rows(p, x.n, 0, lane, up, nullptr);   // (a segment may begin past tile 0)
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int t = 32 * w + lane;
+            zero |= (unsigned long long)__ballot_sync(0xffffffffu, t < tk.count && up[tk.first + t] == kAbsent)
+                    << (32 * w);
+          }
+        }
         if (fix) {
           ok = mbar_wait(smem_u32(&bars->tail), tail_ph, wc);
           tail_ph ^= 1;

@@ -50,6 +50,7 @@ struct Problem {
   int C;                // ranges
   int key_tile;         // keys per tile
   int blk_tiles;        // tiles holding the block's own keys: ceil(S / key_tile)
+  int whole_tiles;      // decode: when no unit has more tiles, each goes to a range of its own, uncut
   int unit_cost;        // decode: fixed cost of a unit in tiles, for the split (sched.cuh); 0: none
   long long T_causal;   // block-causal: total tiles (decode computes T on the device)
   const int* causal_pref;  // block-causal: tiles before block b within one (n, h); NB + 1 entries

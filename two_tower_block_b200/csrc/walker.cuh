@@ -94,8 +94,34 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
     const int U = p.B * p.Hkv;
     if (p.unit_cost > 0 && !(least == most && p.C % U == 0)) cost = fixed_cost(T, U, p.C, p.unit_cost);
     T += (long long)U * cost;
+    if (U <= p.C && most <= p.whole_tiles) {
+      // short units: range c is unit c
+      start = end = T;
+      if (c >= U) return;
+      const int nc = c / p.Hkv, hc = c - nc * p.Hkv;
+      int before = 0;   // tiles of a unit, summed over the sequences before nc
+#pragma unroll 1
+      for (int base = 0; base < nc; base += 32) {
+        const int n = base + lane;
+        before += __reduce_add_sync(0xffffffffu, n < nc ? unit_tiles_k(p, clamp_len(p, n, false)) : 0);
+      }
+      const int tn = unit_tiles_k(p, clamp_len(p, nc, false));
+      first = make_unit(p, c, (long long)p.Hkv * before + (long long)hc * tn);
+      start = first.Tu;
+      end = start + tn;
+      return;
+    }
   } else {
     T = p.T_causal;
+    if (p.whole_tiles > 0) {   // (the host has seen that no unit has more, and that there are no more than C)
+      start = end = T;
+      if (c >= p.B * p.Hkv * p.NB) return;
+      const int nh = c / p.NB;
+      first = make_unit(p, c, (long long)nh * p.causal_pref[p.NB] + p.causal_pref[c - nh * p.NB]);
+      start = first.Tu;
+      end = start + first.tiles;
+      return;
+    }
   }
   const int Ce = used_ranges(T, p.C);
   if (c >= Ce) {
