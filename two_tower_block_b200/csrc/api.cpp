@@ -924,10 +924,6 @@ tt_status_t tt_block_attn_block_causal_backward(tt_plan_t plan, const void* q, c
   p.dq = dq;
   p.dk_blk = dk_blk;
   p.dv_blk = dv_blk;
-  const size_t kv_bytes = (size_t)d.batch * d.seq_len * d.num_kv_heads * d.head_dim * sizeof(float);
-  cudaError_t e = cudaMemsetAsync(dk_blk, 0, kv_bytes, s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(dv_blk, 0, kv_bytes, s);
-  if (e != cudaSuccess) return cuda_fail(e, "clearing dk_blk / dv_blk");
   p.err_word = plan->err_word;
   p.wait_limit_ns = (unsigned long long)(d.wait_timeout_us > 0 ? d.wait_timeout_us : 1000000) * 1000ull;
   // tcgen05 backward on sm_100 plans whose shape it covers (TT_BWD_KERNEL=mma_sync selects
@@ -952,6 +948,14 @@ tt_status_t tt_block_attn_block_causal_backward(tt_plan_t plan, const void* q, c
         !encode_bf16(&maps.k_ctx, p.k_ctx, 2, cd, cs, cb) || !encode_bf16(&maps.v_ctx, p.v_ctx, 2, cd, cs, cb) ||
         !encode_bf16(&maps.k_blk, p.k_blk, 3, bd, bs, bb) || !encode_bf16(&maps.v_blk, p.v_blk, 3, bd, bs, bb))
       return fail(TT_ERR_CUDA, "tensor map (backward) encode failed");
+  }
+  // units of one M-tile write their block's gradients, all others add to them
+  cudaError_t e = cudaSuccess;
+  if (!use_tc || p.R > 128) {
+    const size_t kv_bytes = (size_t)d.batch * d.seq_len * d.num_kv_heads * d.head_dim * sizeof(float);
+    e = cudaMemsetAsync(dk_blk, 0, kv_bytes, s);
+    if (e == cudaSuccess) e = cudaMemsetAsync(dv_blk, 0, kv_bytes, s);
+    if (e != cudaSuccess) return cuda_fail(e, "clearing dk_blk / dv_blk");
   }
   prof_mark(plan, 2, s, true);
   e = use_tc ? tt::launch_attn_bwd_tc(p, maps, plan->sm_count, s) : tt::launch_attn_bwd(p, s);

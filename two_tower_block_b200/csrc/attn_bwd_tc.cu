@@ -19,9 +19,9 @@
 //                  and dO read from TMEM (A operands), K and V from shared memory,
 //                  dQ += dS(j) K(j) with dS read from TMEM as a bf16 pair hi + lo
 //   warps 2, 3   block reducer: dK = scale dS^T Q and dV = P^T dO over the item's rows
-//                for the block's own keys (fp32 FMAs on the staged P and dS), added to
-//                dk_blk / dv_blk with fp32 atomics (the unit's M-tiles and the g query
-//                heads of a KV head all contribute)
+//                (all g query heads of the KV head) for the block's own keys, by warp-level
+//                products on the staged P and dS; written to dk_blk / dv_blk, or where a unit
+//                has two M-tiles added with fp32 atomics
 //   warps 4..7   softmax warpgroup of the even tiles, warps 8..11 of the odd tiles
 //                (thread = TMEM lane = row): p, ds, dS hi + lo back over the S buffer
 // TMEM columns: S(b) = [64b, 64b+64), dP(b) = [128+64b, ...) for two buffers b,
@@ -30,8 +30,8 @@
 // At the start of an item warpgroup 0 copies the item's Q rows and warpgroup 1 its
 // dO rows from the TMA-loaded shared tiles into TMEM.
 //
-// dS enters dQ as hi + lo so dq carries only the rounding of the bf16 inputs; the block
-// reducer takes P and dS in fp32.  Every wait is bounded (ptx.cuh: mbar_wait); on a
+// dS enters dQ as hi + lo, and P and dS the block reducer, so the gradients carry only the
+// rounding of the bf16 inputs.  Every wait is bounded (ptx.cuh: mbar_wait); on a
 // timeout the CTA raises the error word, drains what it issued, frees TMEM and returns.
 #include <type_traits>
 
@@ -362,54 +362,83 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == 2 || warp == 3) {
     // ========================================================= block reducer ==
-    // thread t of 64: dims t and t + 64 (D = 128) or dim t (D = 64), every block key
-    const int t = tid - 64;
+    // dK = dS^T Q and dV = P^T dO by m16n8k16 products: 16 block keys x this warp's half of the
+    // dims, 16 rows at a time.  P and dS enter as hi + lo bf16 pairs (their sum is within 2^-17 of the
+    // fp32 value), Q and dO as the bf16 they are.  The fp32 FMAs of one thread per dim took 39 us
+    // an item whatever its context, which bounded windowed layers.
+    const int w = warp - 2;
+    const int gq = lane >> 2, qq = lane & 3;   // fragment coordinates
     uint32_t item_cnt = 0;
     bool ok = true;
     for (int idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x, ++item_cnt) {
       const Item x = item_of(p, idx, MT);
       ok = mbar_wait(smem_u32(&bars->blk_full), item_cnt & 1, wc);
       if (!ok) break;
-      constexpr int ND = D / 64;
-      float dk[ND][kMaxBlk > 16 ? 16 : kMaxBlk], dv[ND][16];
-      const int nkey = p.S;   // block keys (<= 64 on this path), in chunks of 16
-      for (int k0 = 0; k0 < nkey; k0 += 16) {
+      __syncwarp();
+      constexpr int NT = D / 16;        // 8-dim tiles of a warp
+      const int d0 = w * (D / 2);
+      const uint32_t half = (d0 >> 6) * (128 * kRowBytes);
+      for (int k0 = 0; k0 < p.S; k0 += 16) {
+        float dk[NT][4], dv[NT][4];
 #pragma unroll
-        for (int e = 0; e < ND; ++e)
+        for (int n = 0; n < NT; ++n) dk[n][0] = dk[n][1] = dk[n][2] = dk[n][3] = dv[n][0] = dv[n][1] = dv[n][2] = dv[n][3] = 0.f;
+        // (rows past the M-tile's own: P and dS are 0 there, but shared memory may hold anything)
+#pragma unroll 1
+        for (int r0 = 0; r0 < x.rows; r0 += 16) {
+          uint32_t ph[4], pl[4], sh_[4], sl[4];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) dk[e][k] = dv[e][k] = 0.f;
-        for (int r = 0; r < x.rows; ++r) {
-          float qv[ND], ov[ND];
-#pragma unroll
-          for (int e = 0; e < ND; ++e) {
-            // element (row r, dim d) of a 128-byte-swizzled K-major operand
-            const int d = t + 64 * e;
-            const int hf = d >> 6, c = (d & 63) >> 3;
-            const uint32_t off = hf * (128 * kRowBytes) + r * kRowBytes + ((c ^ (r & 7)) << 4) + (d & 7) * 2;
-            qv[e] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(smem + C::kQOff + off));
-            ov[e] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(smem + C::kOOff + off));
+          for (int i = 0; i < 4; ++i) {
+            const int at = (r0 + 2 * qq + 8 * (i >> 1)) * kStageLd + k0 + gq + 8 * (i & 1);
+            const float p0 = stage_p[at], p1 = stage_p[at + kStageLd], s0 = stage_ds[at], s1 = stage_ds[at + kStageLd];
+            ph[i] = pack_bf16(p0, p1);
+            pl[i] = pack_bf16(p0 - __uint_as_float(ph[i] << 16), p1 - __uint_as_float(ph[i] & 0xFFFF0000u));
+            sh_[i] = pack_bf16(s0, s1);
+            sl[i] = pack_bf16(s0 - __uint_as_float(sh_[i] << 16), s1 - __uint_as_float(sh_[i] & 0xFFFF0000u));
           }
-          const float* ps = stage_p + r * kStageLd + k0;    // same address in every thread
-          const float* ds = stage_ds + r * kStageLd + k0;
+          const int r = r0 + (lane & 7) + 8 * ((lane >> 3) & 1);
+          // of B's words: rows r0 + 2 qq, + 1 (low and high half) and the same + 8
+          const bool tail = r0 + 16 > x.rows;
+          const int ra = r0 + 2 * qq;
+          const uint32_t m0 = (ra < x.rows ? 0xFFFFu : 0u) | (ra + 1 < x.rows ? 0xFFFF0000u : 0u);
+          const uint32_t m1 = (ra + 8 < x.rows ? 0xFFFFu : 0u) | (ra + 9 < x.rows ? 0xFFFF0000u : 0u);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float pv = ps[k], dsv = ds[k];
-#pragma unroll
-            for (int e = 0; e < ND; ++e) {
-              dk[e][k] += dsv * qv[e];
-              dv[e][k] += pv * ov[e];
-            }
+          for (int n2 = 0; n2 < NT / 2; ++n2) {
+            const int c = ((d0 & 63) >> 3) + 2 * n2 + (lane >> 4);
+            const uint32_t off = half + r * kRowBytes + ((c ^ (r & 7)) << 4);
+            uint32_t b0, b1, b2, b3;
+            ldmatrix_x4_trans(q_s + off, b0, b1, b2, b3);
+            if (tail) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
+            mma_bf16_16816(dk[2 * n2], sh_, b0, b1);
+            mma_bf16_16816(dk[2 * n2], sl, b0, b1);
+            mma_bf16_16816(dk[2 * n2 + 1], sh_, b2, b3);
+            mma_bf16_16816(dk[2 * n2 + 1], sl, b2, b3);
+            ldmatrix_x4_trans(o_s + off, b0, b1, b2, b3);
+            if (tail) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
+            mma_bf16_16816(dv[2 * n2], ph, b0, b1);
+            mma_bf16_16816(dv[2 * n2], pl, b0, b1);
+            mma_bf16_16816(dv[2 * n2 + 1], ph, b2, b3);
+            mma_bf16_16816(dv[2 * n2 + 1], pl, b2, b3);
           }
         }
+        // one M-tile: the only contribution; two: each adds its own (to 0, so their order is of no account)
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const int key = k0 + k;
-          if (key < nkey) {
-            const size_t row = ((size_t)(x.n * p.N + x.tok0 + key) * p.Hkv + x.h) * D;
+        for (int h = 0; h < 2; ++h) {
+          const int key = k0 + gq + 8 * h;
+          if (key < p.S) {
+            const size_t at = ((size_t)(x.n * p.N + x.tok0 + key) * p.Hkv + x.h) * D + d0 + 2 * qq;
 #pragma unroll
-            for (int e = 0; e < ND; ++e) {
-              atomicAdd(p.dk_blk + row + t + 64 * e, p.scale * dk[e][k]);
-              atomicAdd(p.dv_blk + row + t + 64 * e, dv[e][k]);
+            for (int n = 0; n < NT; ++n) {
+              const float2 gk = make_float2(p.scale * dk[n][2 * h], p.scale * dk[n][2 * h + 1]);
+              const float2 gv = make_float2(dv[n][2 * h], dv[n][2 * h + 1]);
+              float2* tk = reinterpret_cast<float2*>(p.dk_blk + at + 8 * n);
+              float2* tv = reinterpret_cast<float2*>(p.dv_blk + at + 8 * n);
+              if (MT == 1) {
+                *tk = gk;
+                *tv = gv;
+              } else {
+                atomicAdd(tk, gk);
+                atomicAdd(tv, gv);
+              }
             }
           }
         }
