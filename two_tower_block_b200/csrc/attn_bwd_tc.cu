@@ -461,21 +461,40 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = 128 * x.m + row;                     // packed row of the unit
       const int tt = r / p.g, jj = r - (r / p.g) * p.g;  // block token, query head within the group
       float lse2 = 0.f, delta = 0.f;
-      size_t qrow = 0;
-      if (valid) {
-        qrow = ((size_t)(x.n * p.N + x.tok0 + tt) * p.Hq + x.h * p.g + jj) * D;
-        lse2 = p.lse[(size_t)(x.n * p.Hq + x.h * p.g + jj) * p.N + x.tok0 + tt] * 1.4426950408889634f;
-        const float4* o4 = reinterpret_cast<const float4*>(p.out + qrow);
-        const uint2* d4 = reinterpret_cast<const uint2*>(p.dout + qrow);
-        float acc = 0.f;
-#pragma unroll 4
-        for (int c = 0; c < D / 4; ++c) {
-          const float4 o = o4[c];
-          const uint2 dd = d4[c];
-          acc += o.x * __uint_as_float(dd.x << 16) + o.y * __uint_as_float(dd.x & 0xFFFF0000u) +
-                 o.z * __uint_as_float(dd.y << 16) + o.w * __uint_as_float(dd.y & 0xFFFF0000u);
+      const size_t unit_row = ((size_t)(x.n * p.N + x.tok0) * p.Hq + x.h * p.g) * D;   // of packed row 0
+      const int rel = (tt * p.Hq + jj) * D;
+      const size_t qrow = unit_row + rel;
+      if (valid) lse2 = p.lse[(size_t)(x.n * p.Hq + x.h * p.g + jj) * p.N + x.tok0 + tt] * 1.4426950408889634f;
+      // Delta = dO . out of the warp's 32 rows, whole rows at a time (a thread per row took 15 us an
+      // item for its strided reads), kBatch rows in flight
+      {
+        constexpr int kBatch = 8, kLanes = D / 4;   // lanes of a row: four columns each
+        constexpr int kPer = 32 / kLanes;           // rows of one access
+        const int sub = lane / kLanes, c4 = lane % kLanes;
+#pragma unroll 1
+        for (int j0 = 0; j0 < 32; j0 += kBatch * kPer) {
+          if (q4 * 32 + j0 >= x.rows) break;
+          float4 o[kBatch];
+          uint2 dd[kBatch];
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            const int from = j0 + j * kPer + sub;      // lane (and row of the warp) it is for
+            const size_t at = unit_row + __shfl_sync(0xffffffffu, rel, from) + 4 * c4;
+            const bool there = q4 * 32 + from < x.rows;
+            o[j] = there ? *reinterpret_cast<const float4*>(p.out + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+            dd[j] = there ? *reinterpret_cast<const uint2*>(p.dout + at) : make_uint2(0u, 0u);
+          }
+#pragma unroll
+          for (int j = 0; j < kBatch; ++j) {
+            float acc = o[j].x * __uint_as_float(dd[j].x << 16) + o[j].y * __uint_as_float(dd[j].x & 0xFFFF0000u) +
+                        o[j].z * __uint_as_float(dd[j].y << 16) + o[j].w * __uint_as_float(dd[j].y & 0xFFFF0000u);
+#pragma unroll
+            for (int e = kLanes / 2; e > 0; e >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, e);
+            const int mine = lane - j0 - j * kPer;     // 0 .. kPer - 1: one of these rows is this lane's
+            const float got = __shfl_sync(0xffffffffu, acc, kPer == 1 ? 0 : (mine & 1) * kLanes);
+            if (mine >= 0 && mine < kPer) delta = got;
+          }
         }
-        delta = acc;
       }
       const float2 c2 = make_float2(p.scale_log2, p.scale_log2);
       const float2 nl2 = make_float2(-lse2, -lse2), nd2 = make_float2(-delta, -delta);
@@ -592,12 +611,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       float* dst = p.dq + qrow + (D / 2) * w;
+      const bool wide = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
 #pragma unroll
       for (int cc = 0; cc < D / 64; ++cc) {
         uint32_t o[32];
         tmem_ld32(dq_addr + 32 * cc, o);
         tc_wait_ld();
-        if (valid) {
+        if (valid && wide) {   // whole sectors
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            float f[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) f[k] = p.scale * __uint_as_float(o[8 * q + k]);
+            store_f32x8(dst + 32 * cc + 8 * q, f);
+          }
+        } else if (valid) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             reinterpret_cast<float4*>(dst + 32 * cc)[q] =

@@ -245,6 +245,12 @@ __device__ __forceinline__ unsigned ld_acquire_gpu_u32(const unsigned* a) {
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
   return v;
 }
+// Eight floats to a 32-byte aligned address: a whole sector from one lane.
+__device__ __forceinline__ void store_f32x8(float* p, const float* f) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
 // Add to a counter, after everything this thread has written or seen written.
 __device__ __forceinline__ void red_release_gpu_add(unsigned* a, unsigned v) {
   asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(a), "r"(v) : "memory");
