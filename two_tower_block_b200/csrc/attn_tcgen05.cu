@@ -74,6 +74,7 @@ constexpr float kNoKey = -1e30f;            // reference maximum of a row that h
 
 template <int D, int NK, bool MX = false, bool SPLIT = false>
 struct Cfg {
+  static constexpr int kTreeBytes = kMaxRows * (8 + 2);          // what a tree's rows see, and its walk
   static constexpr int kRows = SPLIT ? 128 : kMaxRows;          // rows of Q in shared memory
   static constexpr int kThreads = MX ? 512 : 384;
   static constexpr int kHalves = D / 64;
@@ -84,7 +85,7 @@ struct Cfg {
   static constexpr int kQBytes = kRows * kRowBytes * kHalves;
   static constexpr int kStageOff = kQBytes;
   static constexpr int kEpiOff = kStageOff + kStages * kSlotBytes;
-  static constexpr int kEpiBytes = 8 * 32 * 32 * 4;  // 8 softmax warps x 32 rows x 32 fp32
+  static constexpr int kEpiBytes = 8 * kTreeBytes;   // scratch of the 8 softmax warps
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
   static constexpr int kBarBytes = 896;
   // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
@@ -95,7 +96,7 @@ struct Cfg {
   static constexpr int kScaleBytes = NK * (D / kMxBlock) + 16;
   static constexpr int kRawMask = kRawScale + 2 * kScaleBytes;
   static constexpr int kRawBytes = kRawMask + 16;
-  static constexpr int kRaw = MX ? (D == 128 ? 3 : 6) : 0;
+  static constexpr int kRaw = MX ? (D == 128 ? 4 : 6) : 0;
   static constexpr int kSmemBytes = kRawOff + kRaw * kRawBytes + 1024;  // + alignment slack
   // Register split: the 128-key variant keeps a full 128-score row per softmax thread (launch: 168
   // per thread = 65536 / 384 rounded down to 8); with converter warps the launch gives 128 and
@@ -140,7 +141,7 @@ static_assert(sizeof(Bars) + sizeof(Shared) <= 896, "barrier block overflows its
 // i-th of the unit's n ranges.  No CTA waits for ranges outside its units.  The waits
 // are bounded; a CTA that gave up (or whose pipeline aborted) combines nothing and the error
 // word says so.
-template <int D, int THREADS>
+template <int D, int THREADS, int kGroup>
 __device__ __forceinline__ void fused_combine(const Problem& p, long long T, long long start, long long end,
                                               const Unit& first, const Unit& last, unsigned k, bool aborted) {
   __shared__ int s_ok;
@@ -159,10 +160,11 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const int c0 = range_of_tile_tab(tab, T, Ce, first_tile(x)), c1 = range_of_tile_tab(tab, T, Ce, end_tile(x) - 1);
     if (warp == 0) {
       bool ok = true;
-      const unsigned long long t0 = timer_start();
+      unsigned long long t0 = globaltimer_ns();
+      bool anew = false;
       for (int cc = c0 + lane; cc <= c1 && ok; cc += 32) {
         while (ld_acquire_gpu_u32(p.arrivals + cc) < k) {
-          if (timer_over(t0, p.wait_limit_ns)) {
+          if (timer_over(t0, p.wait_limit_ns, anew)) {
             raise_error(p.err_word, kErrTimeout);
             ok = false;
             break;
@@ -178,7 +180,7 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const SplitRecord rec{x.u, c1, first_after(x, range_start_tab(tab, T, Ce, c0)) ? 0 : 1, 0};
     const int items = combine_items<D>(p), share = ceil_div(items, n);
 #pragma unroll 1
-    for (int it = i * share + tid; it < min(items, (i + 1) * share); it += THREADS) combine_item<D>(p, x, c0, rec, it);
+    for (int it = i * share + tid; it < min(items, (i + 1) * share); it += THREADS) combine_item<D, kGroup>(p, x, c0, rec, it);
   }
 }
 
@@ -369,7 +371,6 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   const uint32_t q_s = sbase;
   const uint32_t kv_s = sbase + C::kStageOff;
-  float* epi = reinterpret_cast<float*>(smem + C::kEpiOff);
   Bars* bars = reinterpret_cast<Bars*>(smem + C::kBarOff);
   Shared* sh = reinterpret_cast<Shared*>(smem + C::kBarOff + sizeof(Bars));
 
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
 
   const uint32_t tmem = sh->tmem_base;
   const long long T = sh->T, start = sh->start, end = sh->end;
-  const WaitCtx wc{&sh->abort_flag, p.err_word, p.wait_limit_ns};
+  const WaitCtx wc{&sh->abort_flag, p.err_word, p.wait_limit_ns, MX};
   const bool have_work = start < end;
   if constexpr (C::kSplitRegs) {
     if (have_work && warp < 4) regs_dec<C::kCtrlRegs>();
@@ -710,14 +711,14 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
     const int row = q4 * 32 + lane;      // row within the M-tile
     const int mr = SPLIT ? 0 : m;        // M-tile of the rows
     const int r = mr * 128 + row;        // packed row of the unit
-    const bool rows_here = mr * 128 + q4 * 32 < p.R;   // a warp without rows only keeps the barriers going
+    const bool rows_here = !SPLIT || q4 * 32 < p.R;    // a warp without rows only keeps the barriers going
     constexpr int kStep = SPLIT ? 2 : 1;
     if (m < NS) {
       const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
       const uint32_t s_base = tmem + lane_off + m * 128;  // + buffer * NK
       const uint32_t o_addr = tmem + lane_off + 256 + m * D;
-      float* stage = epi + (warp - 4) * 32 * 32;
-      unsigned long long* tree_sees = reinterpret_cast<unsigned long long*>(stage);      // [S <= 256]
+      uint8_t* scratch = smem + C::kEpiOff + (warp - 4) * C::kTreeBytes;
+      unsigned long long* tree_sees = reinterpret_cast<unsigned long long*>(scratch);    // [S <= 256]
       short* tree_up = reinterpret_cast<short*>(tree_sees + kMaxRows);                     // [S]
       const uint32_t gm = div_by(p.g);
       uint32_t G = 0, seg_cnt = 0;
@@ -730,7 +731,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         bool absent = false;
         const int tok = VIS ? row_token(min(r, p.R - 1), gm) : 0;
         if constexpr (VIS) {
-          if (p.parents) {   // (the warp's staging rows are free until the epilogue)
+          if (p.parents) {
             tree_rows(p, x.n, 0, lane, tree_up, tree_sees);
             absent = tree_up[tok] == kAbsent;
           }
@@ -840,17 +841,16 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         const float inv = none ? 0.f : 1.f / l;
         wa *= inv;
         wb *= inv;
-        const int rbase = mr * 128 + q4 * 32;  // first packed row of this warp
-        // element offsets of the rows that this lane stores of a final output (every fourth) from the
-        // unit's first row
-        const size_t at0 = ((size_t)x.ns * p.S * p.Hq + x.h * p.g) * D + (lane & 7) * 4;
-        int at[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int gr = min(rbase + k * 4 + (lane >> 3), p.R - 1);
-          const int t = row_token(gr, gm);
-          at[k] = (t * p.Hq + (gr - t * p.g)) * D;
+        // the lane's row of the final output, as an element offset; a lane writes it 32 bytes, whole
+        // sectors, at a time.  Staging 32 x 32 blocks in shared memory for stores of 128 bytes a row
+        // costs the load-store unit less (a block-causal call with a window of 64: 294 against 320 us),
+        // but 0.5 us of every small call and, by its code, 40 us of 900 with a window of 1024.
+        size_t row_at;
+        {
+          const int gr = min(r, p.R - 1), t = row_token(gr, gm);
+          row_at = ((size_t)(x.ns * p.S + t) * p.Hq + x.h * p.g + (gr - t * p.g)) * D;
         }
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         float* part = p.part_o + part_at(p, sg.slot, r, 0, D);   // four columns on: 4 R floats further
         constexpr int kChunks = D / 32 / kStep;   // SPLIT: this warpgroup's half of the columns
         const int c_lo = SPLIT ? m * kChunks : 0;
@@ -882,30 +882,24 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k) o[k] = 0u;
           }
-          auto four = [&](int q) {
-            return make_float4(__uint_as_float(o[4 * q]), __uint_as_float(o[4 * q + 1]), __uint_as_float(o[4 * q + 2]),
-                               __uint_as_float(o[4 * q + 3]));
-          };
-          if (!sg.full) {
-            if (r < p.R) {
+          if (r < p.R) {
+            if (!sg.full) {
 #pragma unroll
               for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<float4*>(part + (size_t)(cc * 8 + q) * 4 * p.R) = four(q);
+                *reinterpret_cast<uint4*>(part + (size_t)(cc * 8 + q) * 4 * p.R) =
+                    make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+            } else if (p.out_bf16) {
+              uint32_t* to = reinterpret_cast<uint32_t*>(reinterpret_cast<__nv_bfloat16*>(p.out) + row_at + cc * 32);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = pack_bf16(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]));
+#pragma unroll
+              for (int q = 0; q < 2; ++q) store_row(to + 8 * q, o + 8 * q, wide);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                store_row(reinterpret_cast<uint32_t*>(p.out + row_at + cc * 32 + 8 * q), o + 8 * q, wide);
             }
-            continue;
           }
-          // stage the 32x32 block (16-byte chunks XOR-swizzled by row) for coalesced stores
-#pragma unroll
-          for (int q = 0; q < 8; ++q) reinterpret_cast<float4*>(stage + lane * 32)[q ^ (lane & 7)] = four(q);
-          __syncwarp();
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = k * 4 + (lane >> 3);  // row within the warp's 32
-            const int q = lane & 7;
-            if (rbase + rr < p.R)
-              store_out4(p, at0 + at[k] + cc * 32, reinterpret_cast<const float4*>(stage + rr * 32)[q ^ (rr & 7)]);
-          }
-          __syncwarp();
         }
         if (r < p.R && (!SPLIT || m == 0)) {
           const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * 0.6931471805599453f;
@@ -942,7 +936,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, 512);
   if (p.arrivals != nullptr)
-    fused_combine<D, kThreads>(p, T, start, end, sh->first, sh->last, sh->arrival,
+    fused_combine<D, kThreads, C::kSplitRegs ? 4 : 8>(p, T, start, end, sh->first, sh->last, sh->arrival,
                                *(volatile int*)&sh->abort_flag != 0);
 }
 

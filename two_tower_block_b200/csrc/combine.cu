@@ -1,5 +1,5 @@
 // Log-sum-exp combine of the units that a range boundary cut into segments
-// (combine_row.cuh: one thread per four columns of a row), and the bounded-wait self test.
+// (combine_row.cuh: one thread per eight columns of a row), and the bounded-wait self test.
 #include "combine_row.cuh"
 #include "problem.h"
 #include "ptx.cuh"
@@ -8,7 +8,7 @@
 namespace tt {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
@@ -66,7 +66,7 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   // a programmatic dependent launch: the launch overlaps the attention kernel's tail and the
   // kernel waits for the attention grid on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.C, (p.R * (p.D / 4) + kThreads - 1) / kThreads, 1);
+  cfg.gridDim = dim3(p.C, (p.R * (p.D / 8) + kThreads - 1) / kThreads, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -21,20 +21,19 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-// The start of a bounded wait, and whether it has run past its limit.  Nothing promises that the two
-// halves of the timer are read at once: a read across a carry may be 4.3 s off, so the start is taken
-// from two reads that agree, and the limit must be seen passed twice.
-__device__ __forceinline__ unsigned long long timer_start() {
-  unsigned long long a = globaltimer_ns(), b = globaltimer_ns();
-  for (int k = 0; k < 4 && b - a > 1000000ull; ++k) {
-    a = b;
-    b = globaltimer_ns();
+// Whether a bounded wait that began at t0 has run past its limit.  Nothing promises that the two halves
+// of the timer are read at once: a read across a carry may be 4.3 s off.  A waiting thread looks
+// every few microseconds, so a time far past the limit is such a read (or the thread was not
+// running): the wait begins anew then, once.
+__device__ __forceinline__ bool timer_over(unsigned long long& t0, unsigned long long limit_ns, bool& anew) {
+  const unsigned long long now = globaltimer_ns();
+  if ((long long)(now - t0) <= (long long)limit_ns) return false;
+  if (!anew && now - t0 > limit_ns + 1000000000ull) {
+    anew = true;
+    t0 = now;
+    return false;
   }
-  return b;
-}
-__device__ __forceinline__ bool timer_over(unsigned long long t0, unsigned long long limit_ns) {
-  return (long long)(globaltimer_ns() - t0) > (long long)limit_ns &&
-         (long long)(globaltimer_ns() - t0) > (long long)limit_ns;
+  return true;
 }
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -148,8 +147,7 @@ __device__ __forceinline__ bool mbar_try_wait_for(uint32_t bar, uint32_t parity,
       : "memory");
   return ok != 0;
 }
-// Waiting warps suspend rather than poll: polling ones take issue slots from the working ones of
-// their SM sub-partition.
+// What a suspending wait asks for (WaitCtx: suspend).
 constexpr uint32_t kSuspendNs = 20000;
 
 // Context of a bounded wait: a CTA-wide abort flag in shared memory, the
@@ -158,6 +156,10 @@ struct WaitCtx {
   volatile int* abort_flag;
   unsigned* err_word;
   unsigned long long limit_ns;
+  // Suspend rather than poll: polling warps take issue slots from the working ones of their SM
+  // sub-partition, which the 16 warps over a quantised cache feel (one token at B=8, L=65536: 189
+  // -> 184 us), but a suspended warp wakes later (8 16-token blocks over 4096: 33.8 -> 35.8 us).
+  bool suspend = false;
 };
 
 // Wait for the phase of `bar` with parity `parity` to complete.  Returns false
@@ -165,12 +167,13 @@ struct WaitCtx {
 // ran past its limit, in which case it raises kErrTimeout and aborts the CTA.
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const WaitCtx& w) {
   if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = timer_start();
+  unsigned long long t0 = globaltimer_ns();
+  bool anew = false;
   for (uint32_t it = 1;; ++it) {
-    if (mbar_try_wait_for(bar, parity, kSuspendNs)) return true;
+    if (w.suspend ? mbar_try_wait_for(bar, parity, kSuspendNs) : mbar_try_wait(bar, parity)) return true;
     if ((it & 15u) == 0u) {
       if (*w.abort_flag) return false;
-      if (timer_over(t0, w.limit_ns)) {
+      if (timer_over(t0, w.limit_ns, anew)) {
         raise_error(w.err_word, kErrTimeout);
         *w.abort_flag = 1;
         return false;
@@ -244,6 +247,17 @@ __device__ __forceinline__ unsigned ld_acquire_gpu_u32(const unsigned* a) {
   unsigned v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(a) : "memory");
   return v;
+}
+// Eight words to 16-byte aligned (wide: 32-byte aligned, then a whole sector from one lane) memory.
+__device__ __forceinline__ void store_row(uint32_t* p, const uint32_t* w, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 // Eight floats to a 32-byte aligned address: a whole sector from one lane.
 __device__ __forceinline__ void store_f32x8(float* p, const float* f) {
@@ -385,12 +399,13 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
 // Bounded wait with acquire at cluster scope (for barriers other CTAs arrive on).
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, const WaitCtx& w) {
   if (mbar_try_wait_cluster(bar, parity)) return true;
-  const unsigned long long t0 = timer_start();
+  unsigned long long t0 = globaltimer_ns();
+  bool anew = false;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait_cluster(bar, parity)) return true;
     if ((it & 15u) == 0u) {
       if (*w.abort_flag) return false;
-      if (timer_over(t0, w.limit_ns)) {
+      if (timer_over(t0, w.limit_ns, anew)) {
         raise_error(w.err_word, kErrTimeout);
         *w.abort_flag = 1;
         return false;
