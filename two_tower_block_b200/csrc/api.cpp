@@ -317,7 +317,8 @@ bool whole_units_fit(const tt_block_attn_desc& d, const tt::Problem& p) {
 long long most_unit_tiles(const tt::Problem& p) {
   const long long most = p.blk_tiles + (long long)tt::ceil_div(p.ctx_stride, p.key_tile);
   if (p.window <= 0) return most;
-  return std::min(most, p.blk_tiles + 4 + (long long)p.window / p.key_tile + p.sinks / p.key_tile);
+  // (two runs: a partial tile of the sinks, and a window run that may begin up to a slice early)
+  return std::min(most + 2, p.blk_tiles + 4 + (long long)p.window / p.key_tile + p.sinks / p.key_tile);
 }
 
 // The context of a decode call: contiguous slabs, or pages; bf16, or e4m3 with scales.
