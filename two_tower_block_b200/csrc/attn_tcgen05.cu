@@ -81,7 +81,7 @@ struct Cfg {
   static constexpr int kBufs = 128 / NK;                       // S buffers per M-tile
   static constexpr int kSlotBytes = NK * kRowBytes * kHalves;  // one K or V tile
   // the ring: 128 KB, or what fits beside raw tiles
-  static constexpr int kStages = (!MX ? 128 : SPLIT ? 96 : 64) * 1024 / kSlotBytes;
+  static constexpr int kStages = (MX ? 64 : 128) * 1024 / kSlotBytes;
   static constexpr int kQBytes = kRows * kRowBytes * kHalves;
   static constexpr int kStageOff = kQBytes;
   static constexpr int kEpiOff = kStageOff + kStages * kSlotBytes;
@@ -106,9 +106,13 @@ struct Cfg {
   static_assert(4 * 32 * (kCtrlRegs + (MX ? kConvRegs : 0)) + 8 * 32 * kSoftmaxRegs <= kThreads * (MX ? 128 : 168),
                 "register split");
   static_assert(kStages <= 16 && kRaw <= 6, "ring too deep");
-  // SPLIT: a consumer waits for every second tile; with at least three slots each of K and V, the use
-  // before the one it waits for has always been filled (a barrier's parity tells only adjacent uses apart)
-  static_assert(!SPLIT || kStages >= 6, "ring too short for two streams");
+  // SPLIT: a consumer waits for every second tile only, and a barrier's parity tells only one use of a slot
+  // from the next, so the use before the one it waits for must be known to be over.  With an even
+  // number of slots each of K and V that use was the consumer's own, or one of an earlier segment,
+  // all of whose K tiles are consumed when this segment's Q has come, and all V tiles when the
+  // accumulators have been read out (which is waited for first).  An odd number would let a wait for a
+  // tile pass while the other consumer's tile before it was still on its way.
+  static_assert(!SPLIT || kStages / 2 % 2 == 0, "two streams need an even number of slots");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -651,9 +655,10 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
       for (int j = j0; j < n && ok; j += kStep, ++G) {
         const int b = G % NBUF;
         const uint32_t ev = H + (tb + j) % H;  // stage of V of tile j
-        ok = kv_wait(tb + j, 1);
+        // (the accumulator first: SPLIT's V slots of the segment before are all free then)
+        if (j == j0) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
+        if (ok) ok = kv_wait(tb + j, 1);
         if (ok) ok = mbar_wait_warp(smem_u32(&bars->p_full[m][b]), (G / NBUF) & 1, wc);
-        if (ok && j == j0) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
         if (!ok) break;
         tc_fence_after();
         const int nv = round16(tile_keys(p, x, sg.lo + j).count);
