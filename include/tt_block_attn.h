@@ -439,6 +439,16 @@ TT_API const char* tt_status_string(tt_status_t status);
 /* Detail of the last host-side error on the calling thread ("" if none). */
 TT_API const char* tt_last_error_detail(void);
 
+/* Host-only view of the copies that bring in one tile's scale bytes of a quantised cache (no GPU needed):
+ * the tile's `count` positions (1..64) lie in slices of min(page_size, 64) rows, slice s at pool row
+ * slice_rows[s] (negative: a page outside the pool, not read); page_size 0 is a contiguous cache with the
+ * tile at row slice_rows[0].  For each of the tile's 64 words, bytes[w] is what is copied of it (0: nothing)
+ * from byte offset at[w] of the scales to byte 4 w of the tile's buffer.  Every offset is a multiple of 4.
+ * *first_row_at is the byte of the buffer at which the scales of the tile's first row lie.  The same code
+ * decides the copies inside the kernel. */
+TT_API tt_status_t tt_debug_mx_scale_words(int head_dim, int page_size, const int* slice_rows, int count,
+                                           long long* at, int* bytes, int* first_row_at);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1131,4 +1131,25 @@ tt_status_t tt_debug_causal_split(int batch, int num_kv_heads, int seq_len, int 
   return TT_OK;
 }
 
+tt_status_t tt_debug_mx_scale_words(int head_dim, int page_size, const int* slice_rows, int count, long long* at,
+                                    int* bytes, int* first_row_at) {
+  if ((head_dim != 64 && head_dim != 128) || !slice_rows || count < 1 || count > 64 || !at || !bytes || !first_row_at)
+    return fail(TT_ERR_INVALID_ARG, "bad arguments");
+  if (page_size != 0) {
+    const tt_status_t st = page_args(1, page_size, 1);
+    if (st != TT_OK) return st;
+  }
+  const bool paged = page_size != 0;
+  const int psh = paged ? std::min(log2_of(page_size), 6) : 6;
+  const int odd = tt::mx_odd(head_dim, paged, slice_rows[0]);
+  *first_row_at = odd * (head_dim / 32);
+  for (int i = 0; i < 64; ++i) {
+    const tt::ScaleWord w = tt::scale_word(i, head_dim, paged, psh, odd, count);
+    const bool copied = w.bytes > 0 && slice_rows[w.slice] >= 0;
+    bytes[i] = copied ? w.bytes : 0;
+    at[i] = copied ? tt::scale_word_at(w, head_dim, psh, slice_rows[w.slice]) : 0;
+  }
+  return TT_OK;
+}
+
 }  // extern "C"

@@ -196,7 +196,6 @@ template <int D, int NK, bool SPLIT>
 __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                                const WaitCtx& wc, int c, int lane) {
   using C = Cfg<D, NK, true, SPLIT>;
-  constexpr int kRowScale = D / kMxBlock;
   const uint8_t* src[2] = {reinterpret_cast<const uint8_t*>(p.k_ctx), reinterpret_cast<const uint8_t*>(p.v_ctx)};
   const uint8_t* scales[2] = {p.k_scale, p.v_scale};
   const long long start = sh->start, end = sh->end;
@@ -235,20 +234,19 @@ __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* s
         for (int kv = 0; kv < 2; ++kv)
           bulk_load(smem_u32(dst) + (kv * NK + (lane << psh)) * D, src[kv] + (size_t)row * D, mine * D, bar);
       }
-      // scale bytes in words of four; of a contiguous head_dim 64 cache the first word may hold the
-      // row in front of the tile's first (the converters skip it), the last word may be half a one
-      const int odd = D == 64 ? __shfl_sync(0xffffffffu, row, 0) & 1 : 0;
+      // scale bytes in words of four (sched.cuh: the converters skip the row in front of an odd tile)
+      const int odd = mx_odd(D, p.page_table != nullptr, (x.n * p.Hkv + x.h) * p.ctx_stride + tk.first);
 #pragma unroll
       for (int e = 0; e < 64; e += 32) {
-        const int r = (e + lane) * 4 / kRowScale - odd;        // first row of the word
-        const int s = p.page_table ? min(max(r, 0) >> psh, 31) : 0;
+        const ScaleWord w = scale_word(e + lane, D, p.page_table != nullptr, psh, odd, tk.count);
+        const int s = min(w.slice, 31);
         const int row_s = __shfl_sync(0xffffffffu, row, s);
         const bool ok_s = __shfl_sync(0xffffffffu, there, s);
-        if (r < tk.count && ok_s) {
+        if (w.bytes > 0 && ok_s) {
+          const size_t at = (size_t)scale_word_at(w, D, psh, row_s);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv)
-            cp_async_4(smem_u32(dst) + C::kRawScale + kv * C::kScaleBytes + (e + lane) * 4,
-                       scales[kv] + ((size_t)(row_s - (s << psh)) + r) * kRowScale, min(4, (tk.count - r) * kRowScale));
+            cp_async_4(smem_u32(dst) + C::kRawScale + kv * C::kScaleBytes + (e + lane) * 4, scales[kv] + at, w.bytes);
         }
       }
       cp_async_mbar_arrive(bar);
@@ -303,7 +301,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       const uint8_t* raw = smem + C::kRawOff + slot * C::kRawBytes;
       const TileKeys tk = tile_keys(p, x, i);
       const int n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
-      const int odd = D == 64 && !p.page_table ? ((x.n * p.Hkv + x.h) * p.ctx_stride + tk.first) & 1 : 0;
+      const int odd = mx_odd(D, p.page_table != nullptr, (x.n * p.Hkv + x.h) * p.ctx_stride + tk.first);
       const uint32_t mask = *reinterpret_cast<const uint32_t*>(raw + C::kRawMask + first_row / 8);
       const uint8_t* in = raw + (kv * NK + first_row + r4) * D + k4 * 16;
       const uint8_t* sc = raw + C::kRawScale + kv * C::kScaleBytes + (first_row + r4 + odd) * kRowScale + (k4 >> 1);

@@ -109,6 +109,30 @@ TT_HD CtxSpan ctx_span(int L, int window, int sinks, int align, int key_tile) {
   return s;
 }
 
+// The scale bytes of a quantised tile (D / 32 a row) are brought in by words of four bytes, aligned on both
+// sides.  With head_dim 64 a word holds two rows: a contiguous cache's tile may begin at an odd row, and
+// its words then begin one row earlier (the scales lie mx_odd rows into the tile's buffer).  A page, and
+// so every slice of a paged tile, begins at an even row.
+TT_HD int mx_odd(int D, bool paged, int row0) { return D == 64 && !paged ? row0 & 1 : 0; }
+struct ScaleWord {
+  int row;     // its first row within the tile (-1: the row in front of the tile)
+  int slice;   // slice of 1 << psh rows it lies in: its rows follow the slice's first pool row
+  int bytes;   // bytes of it that belong to the tile, 0: none
+};
+TT_HD ScaleWord scale_word(int word, int D, bool paged, int psh, int odd, int count) {
+  const int row_bytes = D / 32;
+  ScaleWord w;
+  w.row = word * 4 / row_bytes - odd;
+  w.slice = paged ? w.row >> psh : 0;
+  const int left = (count - w.row) * row_bytes;
+  w.bytes = left < 0 ? 0 : left < 4 ? left : 4;
+  return w;
+}
+// Byte offset of the word, whose slice begins at pool row `slice_row`.
+TT_HD long long scale_word_at(const ScaleWord& w, int D, int psh, int slice_row) {
+  return ((long long)slice_row - (w.slice << psh) + w.row) * (D / 32);
+}
+
 // Per-range record the attention kernel leaves for the combine: the unit that
 // is cut and begins in this range (or -1), the last range touching it, and
 // the slot choice of this range's piece.

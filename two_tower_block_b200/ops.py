@@ -36,7 +36,7 @@ EXPORTED_SYMBOLS = [
     "tt_last_error_detail", "tt_block_attn_noalloc", "tt_selftest_exp2", "tt_kv_append",
     "tt_block_attn_block_causal_backward", "tt_confidence_unmask", "tt_block_attn_paged",
     "tt_debug_causal_split", "tt_block_attn_plan_window", "tt_block_attn_tree", "tt_block_attn_tree_paged",
-    "tt_kv_append_mx", "tt_kv_read_mx", "tt_block_attn_mx",
+    "tt_kv_append_mx", "tt_kv_read_mx", "tt_block_attn_mx", "tt_debug_mx_scale_words",
 ]
 
 
@@ -94,6 +94,7 @@ def lib() -> ctypes.CDLL:
     L.tt_kv_read_mx.argtypes = [vp, cp, vp, vp, i, vp, vp, vp]
     L.tt_block_attn_mx.argtypes = [vp, vp, cp, vp, vp, vp, vp, vp, vp, vp]
     L.tt_debug_causal_split.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
+    L.tt_debug_mx_scale_words.argtypes = [i, i, ip, i, ctypes.POINTER(ctypes.c_longlong), ip, ip]
     L.tt_block_attn_noalloc.argtypes = [ctypes.POINTER(Desc)] + [vp] * 10
     L.tt_selftest_exp2.argtypes = [i, vp, vp, i]
     L.tt_status_string.argtypes = [i]
@@ -681,6 +682,16 @@ def causal_split(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, u
     _check(lib().tt_debug_causal_split(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost,
                                        starts), "tt_debug_causal_split")
     return list(starts)
+
+
+def mx_scale_words(head_dim, page_size, slice_rows, count):
+    """Host-only: the copies of one tile's scale bytes of a quantised cache, as (byte of the buffer, byte
+    offset in the scales, bytes), and the byte of the buffer where its first row's scales lie."""
+    rows = (ctypes.c_int * len(slice_rows))(*slice_rows)
+    at, num, first = (ctypes.c_longlong * 64)(), (ctypes.c_int * 64)(), ctypes.c_int()
+    _check(lib().tt_debug_mx_scale_words(head_dim, page_size, rows, count, at, num, ctypes.byref(first)),
+           "tt_debug_mx_scale_words")
+    return [(4 * w, at[w], num[w]) for w in range(64) if num[w]], first.value
 
 
 def block_attn_noalloc(q, k_ctx, v_ctx, k_blk, v_blk, ctx_lens, out, lse=None, status=None, scale=0.0,
