@@ -1,6 +1,7 @@
 """The quantised cache at its edges: the alignment of its scale copies, and pages outside the pool."""
 import numpy as np
 import pytest
+import torch
 
 from oracle import mx as omx
 from oracle import visibility as vis
@@ -80,3 +81,43 @@ def test_pages_outside_the_pool_read_as_zeros(S, g, D, page_size, window, sinks,
                                     f64(inp.k_blk), f64(inp.v_blk), lens, window, sinks)
     assert_parity(out, ro, "out")
     assert_parity(lse, rl, "lse")
+
+
+@pytest.mark.parametrize("shape", [(2, 0), (0, 0)])
+def test_a_table_without_entries_is_no_slab(shape):
+    """Pages without a single table entry hold no position; without an address for the table the library would
+    take the pools for slabs of the plan's capacity."""
+    values, scales = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.zeros(3, 2, 16, 2, dtype=torch.uint8)
+    table = torch.zeros(shape, dtype=torch.int32)
+    cache = ops.MxCache(values, scales, values.clone(), scales.clone(), page_table=table)
+    assert cache._d.page_table and cache._d.page_table % 4 == 0
+    assert (cache._d.num_pages, cache._d.page_size, cache._d.pages_per_seq) == (3, 16, 0)
+    assert ops.MxCache(values, scales, values.clone(), scales.clone())._d.page_table is None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", [ops.KERNEL_TCGEN05, ops.KERNEL_MMA_SYNC])
+def test_a_cache_without_positions(kernel):
+    from tests.gpu_util import assert_parity, dev, f64
+    from tests.test_parity_mx import i32
+    from two_tower_block_b200.workloads import make_decode
+    B, S, Hq, Hkv, D = 2, 5, 6, 2, 64
+    inp = make_decode(B, S, Hq, Hkv, D, 40, seed=43, ctx_lens=[0, 0])
+    table = torch.zeros(B, 0, dtype=torch.int32, device="cuda")
+    cache = ops.MxCache.empty(1, Hkv, 16, D, page_table=table)
+    plan = ops.Plan(B, Hq, Hkv, D, S, ctx_capacity=4096, kernel=kernel)   # a capacity that the pool does not hold
+    x = dev(inp.q), dev(inp.k_blk), dev(inp.v_blk)
+    ro, rl = vis.block_attn_visible(f64(inp.q), f64(inp.k_ctx), f64(inp.v_ctx), f64(inp.k_blk), f64(inp.v_blk), [0, 0])
+    for lens, status in (([0, 0], ops.TT_OK), ([0, 30], ops.TT_ERR_DEVICE_ARG)):   # 30: clamped to 0
+        out, lse = plan.block_attn_mx(x[0], cache, x[1], x[2], i32(lens), want_lse=True)
+        assert plan.check_status() == status
+        assert_parity(out, ro, "out")
+        assert_parity(lse, rl, "lse")
+    lens = i32([0, 0])
+    plan.kv_append_mx(x[1], x[2], cache, lens)
+    assert plan.check_status() == ops.TT_ERR_DEVICE_ARG and lens.tolist() == [0, 0]
+    assert not cache.k.view(torch.uint8).any() and not cache.k_scale.any()
+    back = [torch.full((B, Hkv, 3, D), 2.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    plan.kv_read_mx(cache, lens, None, *back)
+    plan.check()
+    assert all((b == 2).all() for b in back)

@@ -246,8 +246,10 @@ class MxCache:
             items = [(k, "k", n, "e4m3"), (v, "v", n, "e4m3"), (k_scale, "k_scale", n // 32, "u8"),
                      (v_scale, "v_scale", n // 32, "u8"), (page_table, "page_table", table, "i32")]
             at = _addrs(self._device if self._device >= 0 else None, items)
-        self._d = MxCacheDesc(at[0], at[1], at[2], at[3], at[4] if page_table is not None else None, num_pages,
-                              page_size, pages_per_seq)
+        # (a table without entries has no address, and none means slabs to the library: it gets one that nothing
+        # reads, since no position lies below a capacity of 0)
+        self._d = MxCacheDesc(at[0], at[1], at[2], at[3], None if page_table is None else at[4] if table else 16,
+                              num_pages, page_size, pages_per_seq)
         self._ref = ctypes.byref(self._d)
 
     @classmethod
