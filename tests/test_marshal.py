@@ -44,3 +44,14 @@ def test_odd_want_is_refused():
     assert ops._quick(-1, (X,), ((torch.bfloat16,),)) is None
     with pytest.raises((TypeError, OverflowError)):
         ops._quick(-1, (X,), ((torch.bfloat16, "24"),))
+
+
+@pytest.mark.parametrize("form", ["_quick", "_quick_py"])
+def test_a_copy_on_write_tensor_gets_memory_of_its_own(form):
+    """A lazy clone shares its source's memory until someone writes: the address that a kernel may write to
+    must not be the source's."""
+    source = torch.arange(24, dtype=torch.float32)
+    clone = torch._lazy_clone(source)
+    at = getattr(ops, form)(-1, (clone,), ((torch.float32, 24),))
+    assert at == [clone.data_ptr()] and at != [source.data_ptr()]
+    assert torch.equal(clone, source)

@@ -9,7 +9,8 @@ namespace {
 
 // addresses(device, tensors, want) -> list of data addresses, or None unless every one of `tensors` is a
 // strided torch tensor on CUDA device `device` (-1: the CPU), contiguous, of the dtype and element count
-// that `want` (a sequence as long: (dtype, numel)) gives for it.
+// that `want` (a sequence as long: (dtype, numel)) gives for it.  Addresses are taken as for writing, as
+// Tensor.data_ptr() does: a copy-on-write tensor gets memory of its own before a kernel writes there.
 PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   if (nargs != 3 || !PyLong_Check(args[0]) || !PyTuple_Check(args[1]) || !PyTuple_Check(args[2]) ||
       PyTuple_GET_SIZE(args[1]) != PyTuple_GET_SIZE(args[2])) {
@@ -38,7 +39,7 @@ PyObject* addresses(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
              t.numel() == numel && (t.is_cuda() ? t.get_device() == device : t.is_cpu() && device == -1) &&
              t.is_contiguous();
       if (fits) {
-        PyObject* at = PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.const_data_ptr()));
+        PyObject* at = PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.mutable_data_ptr()));
         if (!at) return nullptr;
         PyList_SET_ITEM(found, i, at);
       }
