@@ -34,6 +34,8 @@
  *     q, k_*, v_* (and the backward's dout) are bf16; out, lse and gradients
  *     are fp32; ctx_lens is int32.  Every tensor pointer must be 16-byte
  *     aligned (the unmasking step's int / float arrays: 4-byte).
+ *   - What a row sees has to be finite: with a NaN or an infinity among the bf16 values that its softmax
+ *     takes in, the row's results are unspecified.  Positions that it does not see may hold anything.
  *   - Calls are asynchronous and ordered on `stream`; none synchronises the
  *     host except tt_block_attn_check and tt_block_attn_profile_read.
  *   - A plan may be used by one stream at a time (it owns scratch memory).
@@ -266,7 +268,8 @@ TT_API tt_status_t tt_kv_read_mx(tt_plan_t plan, const tt_mx_cache* cache, const
                                  const int32_t* starts, int rows, void* k_out, void* v_out, tt_stream_t stream);
 
 /* Decode block attention over the quantised cache: tt_block_attn (or tt_block_attn_paged) with the
- * context's keys and values taken from `cache`; q, k_blk and v_blk stay bf16.
+ * context's keys and values taken from `cache`; q, k_blk and v_blk stay bf16.  A NaN that the cache holds
+ * shows: a NaN in a key makes out and lse NaN in every row that sees it, one in a value its element of out.
  *   parents  NULL: a bidirectional block; otherwise a drafted tree as in tt_block_attn_tree */
 TT_API tt_status_t tt_block_attn_mx(tt_plan_t plan, const void* q, const tt_mx_cache* cache, const void* k_blk,
                                     const void* v_blk, const int32_t* ctx_lens, const int32_t* parents, float* out,

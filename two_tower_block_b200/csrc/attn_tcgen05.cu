@@ -91,7 +91,13 @@ struct Cfg {
   // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
   static constexpr int kTreeOff = kBarOff + kBarBytes;   // a tree's absent rows, for the V tiles
   static constexpr int kMlOff = kTreeOff + kMaxRows * 2;   // SPLIT: (maximum, sum) of each row, [2][2][128]
-  static constexpr int kRawOff = kMlOff + (SPLIT ? 4 * 128 * 8 : 0);
+  // MX: word s % kNanSegs is s + 1 if a K row that segment s of the CTA sees holds a NaN.  The converters are
+  // at most kStages / 2 + 4 tiles, and so segments, ahead of a softmax warp: the scores of its next two tiles
+  // wait for it, and K slots for the scores.
+  static constexpr int kNanOff = kMlOff + (SPLIT ? 4 * 128 * 8 : 0);
+  static constexpr int kNanSegs = 16;
+  static_assert(kStages / 2 + 4 < kNanSegs, "ring of NaN marks");
+  static constexpr int kRawOff = kNanOff + (MX ? kNanSegs * 4 : 0);
   static constexpr int kRawScale = 2 * NK * D;                      // byte offsets within a slot
   static constexpr int kScaleBytes = NK * (D / kMxBlock) + 16;
   static constexpr int kRawMask = kRawScale + 2 * kScaleBytes;
@@ -277,7 +283,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
   const long long start = sh->start, end = sh->end;
   // lane's 16-byte chunk of a row's half: the k4-th, of row r0 + lane / 4
   const int k4 = lane & 3, r4 = lane >> 2;
-  uint32_t k = 0, t = 0;   // raw tiles converted, tiles of the CTA passed
+  uint32_t k = 0, t = 0, seg = 0;   // raw tiles converted, tiles and segments of the CTA passed
   bool ok = true;
   Unit x = sh->first;
   for (; ok;) {
@@ -311,6 +317,8 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       // of a row in lane's order (one half of head_dim 64).  Not longer: the warps of an SM
       // sub-partition run different code, and what is unrolled further is waited for as
       // instruction fetches (a batch of drafted trees: 241 us rolled, 280 with 32 rows at a time).
+      // The look for NaN is two operations a word of four: 16-token blocks over 131072 positions 205 -> 214 us
+      // (looking in the converted pairs or with a second vote: 217 and more).
       const int h0 = C::kHalves == 2 ? r4 & 1 : 0;
       auto chunk_in = [&](int h, int r0) { return in + (h0 ^ h) * 64 + r0 * D; };
       auto chunk_sc = [&](int h, int r0) { return sc + (h0 ^ h) * 2 + r0 * kRowScale; };
@@ -321,14 +329,16 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       for (int rr = 0; rr < n; rr += 16) {
         constexpr int kChunks = 2 * C::kHalves;   // of lane: rows rr + r4 and rr + 8 + r4
         uint4 b[kChunks];
-        uint32_t byte[kChunks], top = 0;
+        uint32_t byte[kChunks], top = 0, nan = 0;
 #pragma unroll
         for (int e = 0; e < kChunks; ++e) {
           b[e] = *reinterpret_cast<const uint4*>(chunk_in(e % C::kHalves, rr + e / C::kHalves * 8));
           byte[e] = *chunk_sc(e % C::kHalves, rr + e / C::kHalves * 8);
           top = max(top, byte[e]);
+          nan |= mx_nan_bits(b[e].x) | mx_nan_bits(b[e].y) | mx_nan_bits(b[e].z) | mx_nan_bits(b[e].w);
         }
-        if (__all_sync(0xffffffffu, ((mask >> rr) & 0xffffu) == 0xffffu && top <= kMxOneFactor)) {
+        nan &= kMxNan;
+        if (__all_sync(0xffffffffu, ((mask >> rr) & 0xffffu) == 0xffffu && max(top, nan) <= kMxOneFactor)) {
 #pragma unroll
           for (int e = 0; e < kChunks; ++e) {
             const int h = e % C::kHalves, r0 = rr + e / C::kHalves * 8;
@@ -345,6 +355,10 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
             uint4 v = *reinterpret_cast<const uint4*>(chunk_in(h, r0));
             const uint32_t vb = *chunk_sc(h, r0);
             if (!((mask >> (r0 + r4)) & 1u)) v = make_uint4(0, 0, 0, 0);
+            // a NaN in K makes NaN of the tile's scores, which the softmax's maximum and rounding pass over: its
+            // warps find the mark instead (one in V needs none)
+            if (kv == 0 && ((mx_nan_bits(v.x) | mx_nan_bits(v.y) | mx_nan_bits(v.z) | mx_nan_bits(v.w)) & kMxNan))
+              reinterpret_cast<volatile uint32_t*>(smem + C::kNanOff)[seg % C::kNanSegs] = seg + 1;
             *chunk_to(h, r0, 0) = mx_to_bf16x8(make_uint2(v.x, v.y), vb);
             *chunk_to(h, r0, 1) = mx_to_bf16x8(make_uint2(v.z, v.w), vb);
           }
@@ -360,6 +374,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
     }
     if (!ok || sg.last) break;
     x = next_unit(p, x);
+    ++seg;
   }
 }
 
@@ -421,6 +436,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
     sh->abort_flag = 0;
     fence_barrier_init();
   }
+  if (MX && tid < C::kNanSegs) reinterpret_cast<uint32_t*>(smem + C::kNanOff)[tid] = 0u;
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&maps.q);
     tma_prefetch_desc(&maps.k_ctx);
@@ -840,6 +856,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         ok = mbar_wait(smem_u32(&bars->o_full[m]), seg_cnt & 1, wc);
         if (!ok) break;
         tc_fence_after();
+        if (MX && reinterpret_cast<volatile uint32_t*>(smem + C::kNanOff)[seg_cnt % C::kNanSegs] == seg_cnt + 1)
+          l = __int_as_float(0x7FFFFFFF);   // a key of every row is NaN
         const bool none = VIS && (absent || l == 0.f);   // no visible key: 0, lse = -inf
         const float inv = none ? 0.f : 1.f / l;
         wa *= inv;

@@ -64,7 +64,7 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
     wsum *= old;
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
-      const float w = l[u] > -INFINITY ? __expf(l[u] - Mn) : 0.f;
+      const float w = l[u] != -INFINITY ? __expf(l[u] - Mn) : 0.f;   // (a NaN segment spoils the row)
       wsum += w;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -75,7 +75,7 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
       }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] *= inv;
   const size_t off = out_offset(p, x, r, D) + 8 * q;

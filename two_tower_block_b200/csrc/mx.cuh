@@ -35,7 +35,17 @@ __device__ __forceinline__ uint2 mx_to_bf16x4(uint32_t w, uint32_t factor) {
   asm("prmt.b32 %0, %1, 0, 0xB3A2;" : "=r"(y) : "r"(w));
   return make_uint2(mul_bf16x2((x << 4) & 0x87F087F0u, factor), mul_bf16x2((y << 4) & 0x87F087F0u, factor));
 }
-// Eight bytes of one scale block -> eight bf16.
+// e4m3's NaN (all seven magnitude bits set) among four bytes: adding one to every byte carries into bit 7 of
+// such a byte, and of no other unless a NaN lies below it.  Non-zero in the bits kMxNan: there is one.
+constexpr uint32_t kMxNan = 0x80808080u;
+__device__ __forceinline__ uint32_t mx_nan_bits(uint32_t w) { return (w + 0x01010101u) ^ w; }
+// The NaNs of a word over the four bf16 that mx_to_bf16x4 makes of it (480 times the scale).
+__device__ __forceinline__ uint2 mx_keep_nan(uint2 v, uint32_t w) {
+  const uint32_t n = (w & 0x7F7F7F7Fu) + 0x01010101u;   // bit 7 of a byte; to bit 0 of its half, times a NaN's bits
+  return make_uint2(v.x | (((n >> 7) & 1u) | ((n << 1) & 0x10000u)) * 0x7FC0u,
+                    v.y | (((n >> 23) & 1u) | ((n >> 15) & 0x10000u)) * 0x7FC0u);
+}
+// Eight bytes of one scale block -> eight bf16, NaN where they are e4m3's.
 __device__ __forceinline__ uint4 mx_to_bf16x8(uint2 w, uint32_t byte) {
   const uint32_t f = mx_factor(byte);
   const uint2 a = mx_to_bf16x4(w.x, f), b = mx_to_bf16x4(w.y, f);
@@ -43,6 +53,10 @@ __device__ __forceinline__ uint4 mx_to_bf16x8(uint2 w, uint32_t byte) {
   if (byte > kMxOneFactor) {
     const uint32_t g = mx_rest(byte);
     r = make_uint4(mul_bf16x2(r.x, g), mul_bf16x2(r.y, g), mul_bf16x2(r.z, g), mul_bf16x2(r.w, g));
+  }
+  if ((mx_nan_bits(w.x) | mx_nan_bits(w.y)) & kMxNan) {
+    const uint2 x = mx_keep_nan(make_uint2(r.x, r.y), w.x), y = mx_keep_nan(make_uint2(r.z, r.w), w.y);
+    r = make_uint4(x.x, x.y, y.x, y.y);
   }
   return r;
 }
