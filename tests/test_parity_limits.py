@@ -1,0 +1,33 @@
+"""Sizes at the edges of what the calls accept."""
+import pytest
+import torch
+
+from oracle import visibility as vis
+from tests.gpu_util import assert_parity, dev, f64
+from tests.test_parity_visibility import i32
+from two_tower_block_b200 import ops
+from two_tower_block_b200.workloads import make_decode, make_paged
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kernel", [ops.KERNEL_TCGEN05, ops.KERNEL_MMA_SYNC])
+@pytest.mark.parametrize("window", [0, 1500])
+def test_a_page_table_of_the_widest_capacity(window, kernel):
+    """2^31 - 16 positions a sequence (a table row of 2^27 - 1 entries): the tile count of the capacity must not
+    pass 32 bits, or long units would be cut with no combine to follow."""
+    B, S, Hq, Hkv, D, L = 1, 4, 8, 1, 64, 3000
+    inp = make_decode(B, S, Hq, Hkv, D, L, seed=61, ctx_lens=[L])
+    pages = make_paged(inp, 16, seed=62)
+    table = torch.zeros(B, (1 << 27) - 1, dtype=torch.int32, device="cuda")
+    small = torch.from_numpy(pages.page_table).cuda()
+    table[:, :small.shape[1]] = small
+    plan = ops.Plan(B, Hq, Hkv, D, S, window=window, kernel=kernel)
+    out, lse = plan.block_attn_paged(dev(inp.q), dev(pages.k_pages), dev(pages.v_pages), table, dev(inp.k_blk),
+                                     dev(inp.v_blk), i32([L]), out=torch.full((B, S, Hq, D), 7.0, device="cuda"),
+                                     want_lse=True)
+    plan.check()
+    ro, rl = vis.block_attn_visible(f64(inp.q), f64(inp.k_ctx), f64(inp.v_ctx), f64(inp.k_blk), f64(inp.v_blk), [L],
+                                    window, 0)
+    assert_parity(out, ro, "out")
+    assert_parity(lse, rl, "lse")

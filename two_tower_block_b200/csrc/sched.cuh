@@ -79,7 +79,8 @@ TT_HD int range_of_tile_tab(const long long* tab, long long T, int C, long long 
   return lo;
 }
 
-TT_HD int ceil_div(int a, int b) { return (a + b - 1) / b; }
+// (a >= 0; unsigned, since the positions of a page table go up to 2^31 - 16)
+TT_HD int ceil_div(int a, int b) { return (int)(((uint32_t)a + (uint32_t)b - 1u) / (uint32_t)b); }
 
 // Number of tiles of a unit whose visible context has L keys.
 TT_HD int unit_tiles(int L, int key_tile) { return 1 + ceil_div(L, key_tile); }
