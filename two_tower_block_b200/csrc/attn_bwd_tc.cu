@@ -67,7 +67,7 @@ struct BwdCfg {
 };
 
 struct BwdBars {
-  uint64_t q_full, q_empty, qo_full, qo_empty, dq_full, dq_empty, blk_full, blk_empty, drain;
+  uint64_t q_full, q_empty, qo_full, qo_empty, dq_full, dq_empty, blk_full, blk_empty, tail, drain;
   uint64_t sd_full[2], ds_full[2];
   uint64_t kv_full[kStages], kv_empty[kStages];
 };
@@ -150,6 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&bars->dq_empty), 256);  // both softmax warpgroups read their half
     mbar_init(smem_u32(&bars->blk_full), 128);
     mbar_init(smem_u32(&bars->blk_empty), 64);
+    mbar_init(smem_u32(&bars->tail), 1);
     mbar_init(smem_u32(&bars->drain), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_u32(&bars->sd_full[b]), 1);
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ============================================================ producer ==
-    uint32_t it_kv = 0, q_it = 0;
+    uint32_t it_kv = 0, q_it = 0, tail_ph = 0;
     bool ok = true;
     for (int idx = blockIdx.x; idx < n_items && ok; idx += gridDim.x) {
       const Item x = item_of(p, idx, MT);
@@ -211,8 +212,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = mbar_wait(smem_u32(&bars->kv_empty[s]), ((it_kv / kStages) & 1) ^ 1, wc);
           if (!ok) break;
           const uint32_t slot = kv_s + s * C::kSlotBytes;
+          // K rows [count, round16(count)) feed the last dQ k-step: such a tile lands on a barrier of its own and
+          // its slot is handed on when they are cleared
+          const bool tail = kv == 0 && (count & 15) != 0;
           if (lane == 0) {
-            const uint32_t bar = smem_u32(&bars->kv_full[s]);
+            const uint32_t bar = smem_u32(tail ? &bars->tail : &bars->kv_full[s]);
             mbar_arrive_expect_tx(bar, bytes);
             for (int hf = 0; hf < C::kHalves; ++hf) {
               const uint32_t dst = slot + hf * (kNK * kRowBytes);
@@ -223,9 +227,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          // K rows [count, round16(count)) feed the last dQ k-step: clear them once landed
-          if (kv == 0 && (count & 15) != 0) {
-            ok = mbar_wait(smem_u32(&bars->kv_full[s]), (it_kv / kStages) & 1, wc);
+          if (tail) {
+            ok = mbar_wait(smem_u32(&bars->tail), tail_ph, wc);
+            tail_ph ^= 1;
             if (!ok) break;
             const int r0 = count, r1 = round16(count);
             const int n16 = (r1 - r0) * 8 * C::kHalves;
@@ -239,6 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&bars->kv_full[s]));
           }
         }
       }
