@@ -57,14 +57,14 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) Mn = fmaxf(Mn, l[u]);
     // (a row that saw no key in any segment has Mn = -inf: every weight stays 0)
-    const float old = M > -INFINITY ? __expf(M - Mn) : 0.f;
+    const float old = M > -INFINITY ? expf(M - Mn) : 0.f;
     M = Mn;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] *= old;
     wsum *= old;
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
-      const float w = l[u] != -INFINITY ? __expf(l[u] - Mn) : 0.f;   // (a NaN segment spoils the row)
+      const float w = l[u] != -INFINITY ? expf(l[u] - Mn) : 0.f;   // (a NaN segment spoils the row)
       wsum += w;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
