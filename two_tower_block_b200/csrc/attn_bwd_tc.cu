@@ -30,7 +30,7 @@
 // At the start of an item warpgroup 0 copies the item's Q rows and warpgroup 1 its
 // dO rows from the TMA-loaded shared tiles into TMEM.
 //
-// dS enters dQ as hi + lo, and P and dS the block reducer, so the gradients carry only the
+// dS enters dQ as hi + lo, P and dS the block reducer in three parts, so the gradients carry only the
 // rounding of the bf16 inputs.  Every wait is bounded (ptx.cuh: mbar_wait); on a
 // timeout the CTA raises the error word, drains what it issued, frees TMEM and returns.
 #include <type_traits>
@@ -119,6 +119,16 @@ __device__ __forceinline__ void tile_range(const BwdProblem& p, const Item& it, 
 }
 
 __device__ __forceinline__ int round16(int x) { return (x + 15) & ~15; }
+
+// Two fp32 values as three bf16 pairs each: every part takes the 8 bits that the ones before it leave, so the
+// three hold all 24 (above bf16's subnormals).
+__device__ __forceinline__ void split3(float a, float b, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16(a, b);
+  a -= __uint_as_float(hi << 16);
+  b -= __uint_as_float(hi & 0xFFFF0000u);
+  mid = pack_bf16(a, b);
+  lo = pack_bf16(a - __uint_as_float(mid << 16), b - __uint_as_float(mid & 0xFFFF0000u));
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -368,8 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2 || warp == 3) {
     // ========================================================= block reducer ==
     // dK = dS^T Q and dV = P^T dO by m16n8k16 products: 16 block keys x this warp's half of the
-    // dims, 16 rows at a time.  P and dS enter as hi + lo bf16 pairs (their sum is within 2^-17 of the
-    // fp32 value), Q and dO as the bf16 they are.  The fp32 FMAs of one thread per dim took 39 us
+    // dims, 16 rows at a time.  P and dS enter as three bf16 parts that hold all 24 bits of the fp32 value (two
+    // would leave 2^-18 of it), Q and dO as the bf16 they are.  The fp32 FMAs of one thread per dim took 39 us
     // an item whatever its context, which bounded windowed layers.
     const int w = warp - 2;
     const int gq = lane >> 2, qq = lane & 3;   // fragment coordinates
@@ -390,15 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         // (rows past the M-tile's own: P and dS are 0 there, but shared memory may hold anything)
 #pragma unroll 1
         for (int r0 = 0; r0 < x.rows; r0 += 16) {
-          uint32_t ph[4], pl[4], sh_[4], sl[4];
+          uint32_t ph[4], pm[4], pl[4], sh_[4], sm[4], sl[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int at = (r0 + 2 * qq + 8 * (i >> 1)) * kStageLd + k0 + gq + 8 * (i & 1);
             const float p0 = stage_p[at], p1 = stage_p[at + kStageLd], s0 = stage_ds[at], s1 = stage_ds[at + kStageLd];
-            ph[i] = pack_bf16(p0, p1);
-            pl[i] = pack_bf16(p0 - __uint_as_float(ph[i] << 16), p1 - __uint_as_float(ph[i] & 0xFFFF0000u));
-            sh_[i] = pack_bf16(s0, s1);
-            sl[i] = pack_bf16(s0 - __uint_as_float(sh_[i] << 16), s1 - __uint_as_float(sh_[i] & 0xFFFF0000u));
+            split3(p0, p1, ph[i], pm[i], pl[i]);
+            split3(s0, s1, sh_[i], sm[i], sl[i]);
           }
           const int r = r0 + (lane & 7) + 8 * ((lane >> 3) & 1);
           // of B's words: rows r0 + 2 qq, + 1 (low and high half) and the same + 8
@@ -414,14 +422,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             ldmatrix_x4_trans(q_s + off, b0, b1, b2, b3);
             if (tail) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
             mma_bf16_16816(dk[2 * n2], sh_, b0, b1);
+            mma_bf16_16816(dk[2 * n2], sm, b0, b1);
             mma_bf16_16816(dk[2 * n2], sl, b0, b1);
             mma_bf16_16816(dk[2 * n2 + 1], sh_, b2, b3);
+            mma_bf16_16816(dk[2 * n2 + 1], sm, b2, b3);
             mma_bf16_16816(dk[2 * n2 + 1], sl, b2, b3);
             ldmatrix_x4_trans(o_s + off, b0, b1, b2, b3);
             if (tail) b0 &= m0, b1 &= m1, b2 &= m0, b3 &= m1;
             mma_bf16_16816(dv[2 * n2], ph, b0, b1);
+            mma_bf16_16816(dv[2 * n2], pm, b0, b1);
             mma_bf16_16816(dv[2 * n2], pl, b0, b1);
             mma_bf16_16816(dv[2 * n2 + 1], ph, b2, b3);
+            mma_bf16_16816(dv[2 * n2 + 1], pm, b2, b3);
             mma_bf16_16816(dv[2 * n2 + 1], pl, b2, b3);
           }
         }
