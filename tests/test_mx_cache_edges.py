@@ -95,6 +95,18 @@ def test_a_table_without_entries_is_no_slab(shape):
     assert ops.MxCache(values, scales, values.clone(), scales.clone())._d.page_table is None
 
 
+@pytest.mark.parametrize("name", ["k", "k_scale", "v", "v_scale", "page_table"])
+def test_a_cache_keeps_its_tensors(name):
+    """The calls use the addresses taken when the cache was made: another tensor put in its place would be
+    ignored, and the old one's memory could go to someone else."""
+    values, scales = torch.zeros(3, 2, 16, 64, dtype=torch.uint8), torch.zeros(3, 2, 16, 2, dtype=torch.uint8)
+    cache = ops.MxCache(values, scales, values.clone(), scales.clone(), page_table=torch.zeros(2, 4, dtype=torch.int32))
+    old = getattr(cache, name)
+    with pytest.raises(AttributeError):
+        setattr(cache, name, old.clone())
+    assert getattr(cache, name) is old
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kernel", [ops.KERNEL_TCGEN05, ops.KERNEL_MMA_SYNC])
 def test_a_cache_without_positions(kernel):

@@ -222,13 +222,14 @@ class Shape:
 class MxCache:
     """A context cache in microscaled e4m3 (the header's tt_mx_cache): values k, v in any 1-byte type
     and scale bytes k_scale, v_scale with the last dimension D / 32.  Slabs [B, Hkv, Lcap, D], or with
-    `page_table` [B, pages_per_seq] pools [num_pages, Hkv, P, D].  Holds the tensors it describes."""
+    `page_table` [B, pages_per_seq] pools [num_pages, Hkv, P, D].  Holds the tensors it describes, whose contents
+    may change but not their memory."""
 
     def __init__(self, k, k_scale, v, v_scale, page_table=None):
         shape = k.shape
         if len(shape) != 4 or shape[3] % 32:
             raise ValueError(f"k: shape {tuple(shape)}, expected four dimensions, the last a multiple of 32")
-        self.k, self.k_scale, self.v, self.v_scale, self.page_table = k, k_scale, v, v_scale, page_table
+        self._tensors = k, k_scale, v, v_scale, page_table
         self.shape = shape
         self._device = k.get_device() if k.is_cuda else -1
         n = k.numel()
@@ -252,6 +253,13 @@ class MxCache:
                               num_pages, page_size, pages_per_seq)
         self._ref = ctypes.byref(self._d)
 
+    # (read-only: the library has the addresses of these tensors; write into them in place, or make another cache)
+    k = property(lambda self: self._tensors[0])
+    k_scale = property(lambda self: self._tensors[1])
+    v = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    page_table = property(lambda self: self._tensors[4])
+
     @classmethod
     def empty(cls, rows_of, kv_heads, positions, head_dim, device="cuda", page_table=None):
         """A new cache of zeros: `rows_of` sequences of `positions` rows, or (with a page table) that
@@ -267,12 +275,13 @@ class MxCache:
         shape = self.shape
         if self._device != plan.device:
             raise ValueError(f"cache: expected on cuda:{plan.device}, got {self.k.device}")
-        if self.page_table is None:
+        page_table = self._tensors[4]
+        if page_table is None:
             want = (s.batch, s.kv_heads, s.ctx_capacity, s.head_dim)
             if shape != want:
                 raise ValueError(f"cache: shape {tuple(shape)}, expected {want}")
-        elif shape[1] != s.kv_heads or shape[3] != s.head_dim or self.page_table.shape[0] != s.batch:
-            raise ValueError(f"cache: pages {tuple(shape)} with a table {tuple(self.page_table.shape)}, expected "
+        elif shape[1] != s.kv_heads or shape[3] != s.head_dim or page_table.shape[0] != s.batch:
+            raise ValueError(f"cache: pages {tuple(shape)} with a table {tuple(page_table.shape)}, expected "
                              f"[num_pages, {s.kv_heads}, P, {s.head_dim}] and [{s.batch}, pages_per_seq]")
         return self._ref
 
