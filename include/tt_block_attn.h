@@ -191,7 +191,9 @@ TT_API tt_status_t tt_block_attn(tt_plan_t plan, const void* q, const void* k_ct
  * owns all buffers, nothing is allocated.  TT_ERR_INVALID_ARG for a bad page_size, negative
  * counts, a NULL pointer that is needed or a misaligned one (16 bytes for the bf16
  * and fp32 tensors, 4 for the int32 arrays); TT_ERR_UNSUPPORTED when a pool or a
- * logical capacity holds 2^31 rows or more. */
+ * logical capacity holds 2^31 rows or more, or the capacities of all sequences, or of 32
+ * sequences over all KV heads, 2^31 key tiles (64 positions) or more, which only sequences
+ * that share pages could fill. */
 TT_API tt_status_t tt_block_attn_paged(tt_plan_t plan, const void* q, const void* k_pages,
                                 const void* v_pages, const int32_t* page_table, int32_t num_pages,
                                 int32_t page_size, int32_t pages_per_seq, const void* k_blk,

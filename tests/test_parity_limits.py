@@ -31,3 +31,21 @@ def test_a_page_table_of_the_widest_capacity(window, kernel):
                                     window, 0)
     assert_parity(out, ro, "out")
     assert_parity(lse, rl, "lse")
+
+
+@pytest.mark.parametrize("B,Hkv,status", [(32, 1, ops.TT_OK), (33, 2, ops.TT_ERR_UNSUPPORTED),
+                                          (64, 1, ops.TT_ERR_UNSUPPORTED)])
+def test_tables_whose_capacities_pass_the_tile_count_are_refused(B, Hkv, status):
+    """Sequences that share pages may have more positions together than a pool has rows; their tiles are counted
+    in 32 bits.  (No table entry is read here: every length is 0.)"""
+    S, D = 4, 64
+    x = [torch.zeros(B, S, h, D, dtype=torch.bfloat16, device="cuda") for h in (Hkv, Hkv, Hkv)]
+    pool = torch.zeros(1, Hkv, 16, D, dtype=torch.bfloat16, device="cuda")
+    table, lens = i32([[0]] * B), i32([0] * B)
+    out = torch.empty(B, S, Hkv, D, device="cuda")
+    plan = ops.Plan(B, Hkv, Hkv, D, S)
+    p = ops._ptr
+    got = ops.lib().tt_block_attn_paged(plan._h, p(x[0]), p(pool), p(pool), p(table), 1, 16, (1 << 27) - 1, p(x[1]),
+                                        p(x[2]), p(lens), p(out), None, ops._stream(plan))
+    assert got == status
+    plan.check()

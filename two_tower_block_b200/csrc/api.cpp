@@ -402,6 +402,12 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
   } else {
     p.ctx_stride = d.ctx_capacity;
   }
+  // the kernels add up the tiles of all sequences, and those of 32 sequences over all heads, in 32 bits
+  // (walker.cuh: find_range), which sequences that share pages could pass
+  const long long most = most_unit_tiles(p);
+  if (most * d.batch > (1ll << 31) - 1 ||
+      (most + kDecodeUnitCost) * d.num_kv_heads * std::min(d.batch, 32) > (1ll << 31) - 1)
+    return fail(TT_ERR_UNSUPPORTED, "key tiles of the sequences' capacities beyond 2^31");
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_ctx = static_cast<const __nv_bfloat16*>(c.k);
   p.v_ctx = static_cast<const __nv_bfloat16*>(c.v);
@@ -414,7 +420,7 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
     p.unit_cost = kDecodeUnitCost;
     // short contexts: a cut costs a partial and its combine, whole units only their own tiles
     if (whole_units_fit(d, p)) p.whole_tiles = kWholeUnitTiles;
-    if (most_unit_tiles(p) <= p.whole_tiles) {   // no length can cut one: nothing to combine
+    if (most <= p.whole_tiles) {   // no length can cut one: nothing to combine
       p.arrivals = nullptr;
       combine = false;
     }

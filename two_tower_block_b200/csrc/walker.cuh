@@ -78,7 +78,7 @@ __device__ __forceinline__ const long long* range_table(const Problem& p) {
 __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T, long long& start,
                                            long long& end, Unit& first) {
   const int lane = threadIdx.x & 31;
-  int cost = 0, t = 0;   // t: tiles of a unit of sequence base + lane (total rows < 2^31: sums fit)
+  int cost = 0, t = 0;   // t: tiles of a unit of sequence base + lane (sums fit: api.cpp, decode_call)
   if (p.mode == kDecode) {
     int tot = 0, least = INT32_MAX, most = 0;
 #pragma unroll 1   // (cold code: short, or its instruction fetches are what a small call waits for)
