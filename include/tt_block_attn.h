@@ -255,7 +255,7 @@ typedef struct {
  * `rows` need not be the plan's block size: a committed block, an accepted draft or a whole prompt.
  * A sequence with counts[n] outside [0, rows], L_n < 0 or no room is left untouched (rows and
  * length) and flagged TT_ERR_DEVICE_ARG; so is a row whose page lies outside the pool (that row
- * only).  Uses the plan's B, Hkv, D (and ctx_capacity for slabs); B <= 65535. */
+ * only).  Uses the plan's B, Hkv, D (and ctx_capacity for slabs). */
 TT_API tt_status_t tt_kv_append_mx(tt_plan_t plan, const void* k_new, const void* v_new, int rows,
                                    const int32_t* counts, const tt_mx_cache* cache, int32_t* ctx_lens, int advance,
                                    tt_stream_t stream);
@@ -265,7 +265,7 @@ TT_API tt_status_t tt_kv_append_mx(tt_plan_t plan, const void* k_new, const void
  * other rows of the outputs are left as they were.  The value is rounded to nearest even (exact
  * above bf16's subnormals); e4m3's NaN reads as NaN.  starts [B] int32 (device) or NULL: 0.
  * A negative start (nothing is read), a length outside [0, capacity] (clamped) and a page outside
- * the pool (its rows are skipped) are flagged TT_ERR_DEVICE_ARG.  B <= 65535. */
+ * the pool (its rows are skipped) are flagged TT_ERR_DEVICE_ARG. */
 TT_API tt_status_t tt_kv_read_mx(tt_plan_t plan, const tt_mx_cache* cache, const int32_t* ctx_lens,
                                  const int32_t* starts, int rows, void* k_out, void* v_out, tt_stream_t stream);
 

@@ -49,3 +49,22 @@ def test_tables_whose_capacities_pass_the_tile_count_are_refused(B, Hkv, status)
                                         p(x[2]), p(lens), p(out), None, ops._stream(plan))
     assert got == status
     plan.check()
+
+
+def test_a_quantised_cache_of_many_sequences():
+    B, D = 70001, 64
+    cache = ops.MxCache.empty(B, 1, 2, D)
+    plan = ops.Plan(B, 1, 1, D, 1, ctx_capacity=2)
+    rows = torch.arange(B, device="cuda").remainder(449).sub(224).to(torch.bfloat16)
+    rows = rows[:, None, None, None].expand(B, 1, 1, D).contiguous()
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    for step in (1, 2):
+        plan.kv_append_mx(rows * step, -rows, cache, lens)
+        assert bool((lens == step).all())
+    k, v = (torch.full((B, 1, 2, D), 9.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    plan.kv_read_mx(cache, lens, None, k, v)
+    plan.check()
+    # equal elements: the scale is a power of two, so each reads as e4m3 of its mantissa, within 2^-4
+    want = rows[:, :, 0].float()
+    for got, ref in ((k[:, :, 0], want), (k[:, :, 1], 2 * want), (v[:, :, 0], -want), (v[:, :, 1], -want)):
+        assert bool(((got.float() - ref).abs() <= 2.0 ** -4 * ref.abs()).all())

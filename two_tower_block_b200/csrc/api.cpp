@@ -441,7 +441,6 @@ tt_status_t mx_rows(tt_plan_t plan, const tt_mx_cache* cache, tt::MxRows* m) {
   }
   if (!plan) return fail(TT_ERR_INVALID_ARG, "null plan");
   const tt_block_attn_desc& d = plan->desc;
-  if (d.batch > 65535) return fail(TT_ERR_UNSUPPORTED, "cache writes and reads take at most 65535 sequences");
   if (cache->page_table) {
     const tt_status_t st = page_range(d, cache->num_pages, cache->page_size, cache->pages_per_seq);
     if (st != TT_OK) return st;
@@ -786,7 +785,7 @@ tt_status_t tt_kv_append_mx(tt_plan_t plan, const void* k_new, const void* v_new
   DeviceGuard guard(plan->device);
   const cudaError_t e =
       tt::launch_kv_append_mx(k_new, v_new, m, ctx_lens, counts, d.batch, rows, advance ? 1 : 0, plan->ticket,
-                              plan->err_word, reinterpret_cast<cudaStream_t>(stream));
+                              plan->err_word, plan->sm_count, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_mx launch");
   return TT_OK;
 }
@@ -804,7 +803,7 @@ tt_status_t tt_kv_read_mx(tt_plan_t plan, const tt_mx_cache* cache, const int32_
     return fail(TT_ERR_INVALID_ARG, "tensor pointer not 16-byte aligned");
   DeviceGuard guard(plan->device);
   const cudaError_t e = tt::launch_kv_read_mx(m, ctx_lens, starts, d.batch, rows, k_out, v_out, plan->err_word,
-                                              reinterpret_cast<cudaStream_t>(stream));
+                                              plan->sm_count, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_read_mx launch");
   return TT_OK;
 }

@@ -172,11 +172,11 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// y: what gives the GPU a few waves of full SMs over all (sequence, head) pairs, at most one block per
-// pass over the rows.
-dim3 grid_of(int T, int B, int Hkv, int D) {
+// x: the (sequence, head) pairs (below 2^31, as the plan's rows are).  y: what gives the GPU four waves of full
+// SMs over them, at most one block per pass over the rows.
+dim3 grid_of(int T, int B, int Hkv, int D, int sms) {
   const long long per = kThreads / (D / 16), pairs = (long long)B * Hkv;
-  const long long want = (T + per - 1) / per, most = (148 * 8 * 4 + pairs - 1) / pairs;
+  const long long want = (T + per - 1) / per, most = (sms * 8 * 4 + pairs - 1) / pairs;
   const long long y = want < most ? want : most;
   return dim3((unsigned)pairs, (unsigned)(y > 0 ? y : 1), 1);
 }
@@ -185,16 +185,16 @@ dim3 grid_of(int T, int B, int Hkv, int D) {
 
 cudaError_t launch_kv_append_mx(const void* k_new, const void* v_new, const MxRows& m, int32_t* ctx_lens,
                                 const int32_t* counts, int B, int T, int advance, unsigned* ticket,
-                                unsigned* err_word, cudaStream_t stream) {
-  const dim3 grid = grid_of(T, B, m.Hkv, m.D);
+                                unsigned* err_word, int sms, cudaStream_t stream) {
+  const dim3 grid = grid_of(T, B, m.Hkv, m.D, sms);
   kv_append_mx_kernel<<<grid, kThreads, 0, stream>>>(static_cast<const uint4*>(k_new), static_cast<const uint4*>(v_new),
                                                      m, ctx_lens, counts, B, T, advance, ticket, err_word);
   return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read_mx(const MxRows& m, const int32_t* ctx_lens, const int32_t* starts, int B, int T,
-                              void* k_out, void* v_out, unsigned* err_word, cudaStream_t stream) {
-  const dim3 grid = grid_of(T, B, m.Hkv, m.D);
+                              void* k_out, void* v_out, unsigned* err_word, int sms, cudaStream_t stream) {
+  const dim3 grid = grid_of(T, B, m.Hkv, m.D, sms);
   kv_read_mx_kernel<<<grid, kThreads, 0, stream>>>(m, ctx_lens, starts, T, static_cast<uint4*>(k_out),
                                                    static_cast<uint4*>(v_out), err_word);
   return cudaGetLastError();

@@ -20,9 +20,9 @@ struct MxRows {
 // launch leaves at zero).
 cudaError_t launch_kv_append_mx(const void* k_new, const void* v_new, const MxRows& m, int32_t* ctx_lens,
                                 const int32_t* counts, int B, int T, int advance, unsigned* ticket,
-                                unsigned* err_word, cudaStream_t stream);
+                                unsigned* err_word, int sms, cudaStream_t stream);
 // Positions [starts[n], starts[n] + T) below ctx_lens[n] as bf16 into [B, Hkv, T, D].
 cudaError_t launch_kv_read_mx(const MxRows& m, const int32_t* ctx_lens, const int32_t* starts, int B, int T,
-                              void* k_out, void* v_out, unsigned* err_word, cudaStream_t stream);
+                              void* k_out, void* v_out, unsigned* err_word, int sms, cudaStream_t stream);
 
 }  // namespace tt
