@@ -13,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -43,6 +44,21 @@ def _marshal_cmd(src):
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
 
 
+def _build_marshal(binding):
+    """The library does without it (ops.py has the same in Python), so a machine without a host compiler, or
+    without Python's or torch's headers, is told and goes on."""
+    try:
+        r = subprocess.run(_marshal_cmd(binding), capture_output=True, text=True)
+        why = r.stderr if r.returncode != 0 else None
+    except (OSError, ImportError) as e:
+        why = str(e)
+    if why is None:
+        os.replace(MARSHAL + ".tmp", MARSHAL)
+    else:
+        sys.stderr.write(why)
+        warnings.warn("the compiled argument marshalling could not be built: the binding's Python form will run")
+
+
 def _headers():
     return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
@@ -64,9 +80,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             cmd += ["-x", "cu" if s.endswith(".cu") else "c++", "-c", s, "-o", o]
             jobs.append(cmd)
 
-    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(binding):
-        jobs.append(_marshal_cmd(binding))
-
     def run(cmd):
         if verbose:
             print(" ".join(cmd), flush=True)
@@ -79,8 +92,6 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
                 raise RuntimeError("build failed: " + " ".join(cmd))
-    if os.path.exists(MARSHAL + ".tmp"):
-        os.replace(MARSHAL + ".tmp", MARSHAL)
     if jobs or force or not os.path.exists(LIB):
         cmd = [nvcc()] + ARCH + ["-shared", "-Xcompiler", "-fPIC", "-o", LIB + ".tmp"] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -88,6 +99,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
+    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(binding):
+        _build_marshal(binding)
     return LIB
 
 
