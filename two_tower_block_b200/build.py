@@ -2,12 +2,13 @@
 
 Usage: python -m two_tower_block_b200.build [--force] [-v]
 Objects go to two_tower_block_b200/_build/; the shared library is written
-next to this file so that it travels with the source tree, and so is _marshal.so,
+next to this file so that it travels with the source tree, and so is _marshal,
 the argument marshalling of the Python binding (the only part that knows torch).
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -21,7 +22,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtt_block_attn.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL = os.path.join(HERE, "_marshal" + sysconfig.get_config_var("EXT_SUFFIX"))   # of this Python's ABI
+MARSHAL_FOR = os.path.join(BUILD, "marshal.torch")   # the torch that it was built against
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
@@ -38,10 +40,30 @@ def _marshal_cmd(src):
     import torch
     t = os.path.dirname(torch.__file__)
     return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
-            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I" + os.path.join(t, "include"),
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DTT_TORCH_VERSION="{torch.__version__}"', "-I" + os.path.join(t, "include"),
             "-I" + os.path.join(t, "include", "torch", "csrc", "api", "include"),
             "-I" + sysconfig.get_paths()["include"], src, "-o", MARSHAL + ".tmp", "-L" + os.path.join(t, "lib"),
             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+
+
+def _torch_version():
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return ""
+
+
+def _marshal_is_current(binding):
+    """Newer than its source, and built against the torch that is installed: it uses torch's classes by their
+    layout."""
+    if not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(binding):
+        return False
+    try:
+        with open(MARSHAL_FOR) as f:
+            return f.read() == _torch_version()
+    except OSError:
+        return False
 
 
 def _build_marshal(binding):
@@ -54,6 +76,8 @@ def _build_marshal(binding):
         why = str(e)
     if why is None:
         os.replace(MARSHAL + ".tmp", MARSHAL)
+        with open(MARSHAL_FOR, "w") as f:
+            f.write(_torch_version())
     else:
         sys.stderr.write(why)
         warnings.warn("the compiled argument marshalling could not be built: the binding's Python form will run")
@@ -99,7 +123,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(LIB + ".tmp", LIB)
-    if force or not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(binding):
+    if force or not _marshal_is_current(binding):
         _build_marshal(binding)
     return LIB
 

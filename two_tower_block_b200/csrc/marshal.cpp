@@ -66,4 +66,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal(void) { return PyModule_Create(&kModule); }
+// built_for: the torch whose headers these classes' layouts were taken from (ops.py asks before the first use).
+PyMODINIT_FUNC PyInit__marshal(void) {
+  PyObject* const m = PyModule_Create(&kModule);
+  if (m && PyModule_AddStringConstant(m, "built_for", TT_TORCH_VERSION) != 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -185,10 +185,19 @@ def _quick_py(device, tensors, want):
     return at
 
 
-try:   # the same in C++ (csrc/marshal.cpp), a tenth of the time; built beside the library
-    from ._marshal import addresses as _quick
+def _pick_quick(module):
+    """The same in C++ (csrc/marshal.cpp), a tenth of the time, where it was built against this very torch: it
+    reads torch's tensors by the layout that it found in the headers."""
+    if getattr(module, "built_for", None) == torch.__version__:
+        return module.addresses
+    return _quick_py
+
+
+try:   # built beside the library
+    from . import _marshal
 except ImportError:
-    _quick = _quick_py
+    _marshal = None
+_quick = _pick_quick(_marshal)
 
 
 def _addrs(device, items):
