@@ -439,6 +439,27 @@ TT_API tt_status_t tt_debug_work_split(int num_units, const int* tiles_per_unit,
 TT_API tt_status_t tt_debug_causal_split(int batch, int num_kv_heads, int seq_len, int block_size,
                                          int key_tile, int num_ctas, int unit_cost, long long* range_start);
 
+/* The same for a plan with a window (tt_block_attn_plan_window; window 0, sinks 0: the above). */
+TT_API tt_status_t tt_debug_causal_split_window(int batch, int num_kv_heads, int seq_len, int block_size,
+                                                int key_tile, int num_ctas, int unit_cost, int window, int sinks,
+                                                long long* range_start);
+
+/* Host-only view of a decode call's work split (no GPU needed): `batch` sequences whose units have
+ * seq_tiles[n] >= 1 key tiles each, num_kv_heads units a sequence, over num_ctas ranges, with the fixed
+ * cost of a unit `unit_cost` (tiles; 0: none) and the length `whole_tiles` up to which units stay whole.
+ *   range_start [num_ctas + 1]   first global place of each range (places: the tiles and the empty
+ *                                places of each unit's cost); ranges that are not used start at the end
+ *   record      [num_ctas][3]    of each range: the cut unit that begins in it (-1: none), the last range
+ *                                that has a piece of it, and which of this range's two slots holds the first
+ *   segment     [max_segments][5] the pieces in order: range, unit, its first tile and the one behind its
+ *                                last, slot (-1: the whole unit, which needs none)
+ *   *cost, *num_segments         the cost that was taken, the pieces found (at most max_segments are written)
+ * The same code decides the split inside the kernels.  TT_ERR_INVALID_ARG for NULL pointers and sizes below 1
+ * (unit_cost, whole_tiles, max_segments: below 0). */
+TT_API tt_status_t tt_debug_decode_split(int batch, const int* seq_tiles, int num_kv_heads, int num_ctas,
+                                         int unit_cost, int whole_tiles, long long* range_start, int* record,
+                                         int max_segments, int* segment, int* cost, int* num_segments);
+
 TT_API const char* tt_status_string(tt_status_t status);
 
 /* Detail of the last host-side error on the calling thread ("" if none). */

@@ -472,6 +472,18 @@ std::vector<long long> causal_range_table(const tt_plan_s* P, const std::vector<
   return weighted_causal_starts(pref, (long long)d.batch * d.num_kv_heads, P->C, H);
 }
 
+// Tiles of one (n, h) before each of its NB blocks, and their sum; false from 2^31 tiles on.
+bool causal_prefix(int NB, int S, int key_tile, int window, int sinks, std::vector<int>& pref) {
+  pref.resize(NB + 1);
+  long long acc = 0;
+  for (int b = 0; b <= NB; ++b) {
+    pref[b] = (int)acc;
+    if (b < NB) acc += tt::ceil_div(S, key_tile) + tt::ctx_span(S * b, window, sinks, 1, key_tile).tiles;
+    if (acc > (1ll << 31) - 1) return false;
+  }
+  return true;
+}
+
 tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int device, tt_plan_t* out_plan) {
   g_detail.clear();
   if (!desc || !out_plan) return fail(TT_ERR_INVALID_ARG, "null descriptor or output pointer");
@@ -554,20 +566,12 @@ tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int
   std::vector<int> pref;
   if (d.seq_len > 0) {
     const int NB = d.seq_len / d.block_size;
-    pref.resize(NB + 1);
-    long long acc = 0;
-    for (int b = 0; b <= NB; ++b) {
-      pref[b] = (int)acc;
-      if (b < NB)
-        acc += tt::ceil_div(d.block_size, P->key_tile) +
-               tt::ctx_span(d.block_size * b, window, sinks, 1, P->key_tile).tiles;
-    }
-    if (acc > (1ll << 31) - 1) {
+    if (!causal_prefix(NB, d.block_size, P->key_tile, window, sinks, pref)) {
       delete P;
       return fail(TT_ERR_UNSUPPORTED, "sequence too long");
     }
     P->causal_NB = NB;
-    P->causal_T = (long long)d.batch * d.num_kv_heads * acc;
+    P->causal_T = (long long)d.batch * d.num_kv_heads * pref[NB];
   }
 
   // Decode calls on the default tcgen05 kernel: with U = batch * Hkv units and at least two
@@ -1116,23 +1120,86 @@ tt_status_t tt_debug_work_split(int num_units, const int* tiles_per_unit, int nu
 
 tt_status_t tt_debug_causal_split(int batch, int num_kv_heads, int seq_len, int block_size, int key_tile,
                                   int num_ctas, int unit_cost, long long* range_start) {
+  return tt_debug_causal_split_window(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost, 0, 0,
+                                      range_start);
+}
+
+tt_status_t tt_debug_causal_split_window(int batch, int num_kv_heads, int seq_len, int block_size, int key_tile,
+                                         int num_ctas, int unit_cost, int window, int sinks, long long* range_start) {
   if (batch < 1 || num_kv_heads < 1 || block_size < 1 || seq_len < block_size || seq_len % block_size != 0 ||
-      key_tile < 1 || num_ctas < 1 || !range_start)
+      key_tile < 1 || num_ctas < 1 || window < 0 || sinks < 0 || (sinks > 0 && window == 0) || !range_start)
     return fail(TT_ERR_INVALID_ARG, "bad arguments");
   const int NB = seq_len / block_size;
-  std::vector<int> pref(NB + 1);
-  long long acc = 0;
-  for (int b = 0; b <= NB; ++b) {
-    pref[b] = (int)acc;
-    if (b < NB) acc += tt::ceil_div(block_size, key_tile) + tt::ceil_div(block_size * b, key_tile);
-    if (acc > (1ll << 31) - 1) return fail(TT_ERR_UNSUPPORTED, "sequence too long");
-  }
-  const long long T = (long long)batch * num_kv_heads * acc;
+  std::vector<int> pref;
+  if (!causal_prefix(NB, block_size, key_tile, window, sinks, pref))
+    return fail(TT_ERR_UNSUPPORTED, "sequence too long");
+  const long long T = (long long)batch * num_kv_heads * pref[NB];
   const std::vector<long long> tab =
       weighted_causal_starts(pref, (long long)batch * num_kv_heads, num_ctas, unit_cost < 0 ? kCausalUnitCost : unit_cost);
   const int Ce = tt::used_ranges(T, num_ctas);
   for (int c = 0; c <= num_ctas; ++c)
     range_start[c] = c > Ce ? T : tab.empty() ? tt::range_start(T, Ce, c) : tab[c];
+  return TT_OK;
+}
+
+tt_status_t tt_debug_decode_split(int batch, const int* seq_tiles, int num_kv_heads, int num_ctas, int unit_cost,
+                                  int whole_tiles, long long* range_start, int* record, int max_segments,
+                                  int* segment, int* cost, int* num_segments) {
+  if (batch < 1 || !seq_tiles || num_kv_heads < 1 || num_ctas < 1 || unit_cost < 0 || whole_tiles < 0 ||
+      !range_start || !record || max_segments < 0 || (max_segments > 0 && !segment) || !cost || !num_segments ||
+      (long long)batch * num_kv_heads > (1ll << 31) - 1)
+    return fail(TT_ERR_INVALID_ARG, "bad arguments");
+  const int U = batch * num_kv_heads;
+  int least = seq_tiles[0], most = seq_tiles[0];
+  long long tot = 0;
+  for (int n = 0; n < batch; ++n) {
+    if (seq_tiles[n] < 1) return fail(TT_ERR_INVALID_ARG, "every unit has at least one tile");
+    least = std::min(least, seq_tiles[n]);
+    most = std::max(most, seq_tiles[n]);
+    tot += seq_tiles[n];
+  }
+  long long T = num_kv_heads * tot;
+  *cost = tt::decode_cost(T, U, num_ctas, unit_cost, least, most);
+  T += (long long)U * *cost;
+  const bool whole = tt::whole_units(U, num_ctas, most, whole_tiles);
+  const int Ce = whole ? U : tt::used_ranges(T, num_ctas);
+  auto unit = [&](int u, long long Tu) {
+    tt::Unit x{};
+    x.u = u;
+    x.tiles = seq_tiles[u / num_kv_heads];
+    x.cost = whole ? 0 : *cost;
+    x.Tu = Tu;
+    return x;
+  };
+  // (whole units: range c begins where unit c does, in places of tiles only)
+  long long end_of_all = T;
+  if (whole) end_of_all = T - (long long)U * *cost;
+  tt::Unit x = unit(0, 0);
+  *num_segments = 0;
+  for (int c = 0; c <= num_ctas; ++c) {
+    range_start[c] = c >= Ce ? end_of_all : whole ? x.Tu : tt::range_start(T, Ce, c);
+    if (c >= Ce) {
+      if (c < num_ctas) record[3 * c] = record[3 * c + 1] = -1, record[3 * c + 2] = 0;
+      continue;
+    }
+    const long long start = range_start[c], end = whole ? start + x.tiles : tt::range_start(T, Ce, c + 1);
+    while (tt::end_tile(x) <= start) x = unit(x.u + 1, x.Tu + x.tiles + x.cost);
+    for (;;) {
+      const tt::Segment s = tt::segment_of(x, start, end, c);
+      if (*num_segments < max_segments) {
+        const int at[5] = {c, x.u, s.lo, s.hi, s.full ? -1 : s.slot};
+        std::copy(at, at + 5, segment + 5 * *num_segments);
+      }
+      ++*num_segments;
+      if (s.last) break;
+      x = unit(x.u + 1, x.Tu + x.tiles + x.cost);
+    }
+    const tt::SplitRecord r = tt::record_of(x, whole ? end_of_all : T, num_ctas, start, end, nullptr);
+    record[3 * c] = r.unit;
+    record[3 * c + 1] = r.last_range;
+    record[3 * c + 2] = r.first_which;
+    if (whole && c + 1 < Ce) x = unit(x.u + 1, x.Tu + x.tiles);
+  }
   return TT_OK;
 }
 

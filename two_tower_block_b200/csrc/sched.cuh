@@ -64,6 +64,14 @@ TT_HD int fixed_cost(long long T, long long U, int C, int want) {
   return most < want ? (int)most : want;
 }
 
+// The cost per unit of a decode call whose units have `least` to `most` tiles: units of one length over ranges
+// that divide them evenly need no weighing.
+TT_HD int decode_cost(long long T, int U, int C, int want, int least, int most) {
+  return want > 0 && !(least == most && C % U == 0) ? fixed_cost(T, U, C, want) : 0;
+}
+// Short units: range c is unit c.
+TT_HD bool whole_units(int U, int C, int most, int whole_tiles) { return U <= C && most <= whole_tiles; }
+
 // The same two for a boundary table (null: the uniform split).
 TT_HD long long range_start_tab(const long long* tab, long long T, int C, int c) {
   return tab ? tab[c] : range_start(T, C, c);
@@ -143,5 +151,63 @@ struct SplitRecord {
   int first_which;
   int pad;
 };
+
+// One unit, as the kernels walk over them.
+struct Unit {
+  int u;          // unit index
+  int tiles;      // number of key tiles
+  int L;          // visible context keys
+  int n, h, b;    // sequence, KV head, block index within the sequence
+  int ns;         // block-sequence index n * NB + b (row block of q / k_blk / out)
+  int sink_tiles, wstart, head;  // context runs of a windowed layer (CtxSpan)
+  int cost;       // its fixed cost, cost / 2 places of it before the tiles
+  long long Tu;   // first global place of the unit
+};
+
+// Global places of the unit's first tile, and behind its last.
+TT_HD long long first_tile(const Unit& x) { return x.Tu + x.cost / 2; }
+TT_HD long long end_tile(const Unit& x) { return first_tile(x) + x.tiles; }
+// Whether no later unit has a tile before `end`, and no earlier one a tile at or after `start`.
+TT_HD bool last_before(const Unit& x, long long end) { return end_tile(x) + x.cost >= end; }
+TT_HD bool first_after(const Unit& x, long long start) {
+  return first_tile(x) - x.cost <= start;
+}
+
+// Segment of the current unit inside [start, end).
+struct Segment {
+  int lo, hi;     // unit-local tiles [lo, hi)
+  bool full;      // covers the whole unit: write the final output
+  int slot;       // partial slot when !full
+  bool last;      // last segment of the range
+};
+
+TT_HD Segment segment_of(const Unit& x, long long start, long long end, int c) {
+  Segment s;
+  const long long f = first_tile(x);
+  s.lo = start > f ? (int)(start - f) : 0;
+  s.hi = end - f < x.tiles ? (int)(end - f) : x.tiles;
+  s.full = (s.lo == 0 && s.hi == x.tiles);
+  s.slot = 2 * c + (s.lo > 0 || first_after(x, start) ? 0 : 1);
+  s.last = last_before(x, end);
+  return s;
+}
+
+// The record of range c: the cut unit that begins in c and runs past its end.
+// C is the plan's range count; the split uses min(C, T) of them.
+TT_HD SplitRecord record_of(const Unit& last, long long T, int C, long long start, long long end,
+                            const long long* tab) {
+  C = used_ranges(T, C);
+  SplitRecord r;
+  r.unit = -1;
+  r.last_range = -1;
+  r.first_which = 0;
+  r.pad = 0;
+  if (first_tile(last) >= start && end_tile(last) > end) {
+    r.unit = last.u;
+    r.last_range = range_of_tile_tab(tab, T, C, end_tile(last) - 1);
+    r.first_which = first_after(last, start) ? 0 : 1;
+  }
+  return r;
+}
 
 }  // namespace tt

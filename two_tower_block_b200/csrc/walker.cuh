@@ -6,17 +6,6 @@
 
 namespace tt {
 
-struct Unit {
-  int u;          // unit index
-  int tiles;      // number of key tiles
-  int L;          // visible context keys
-  int n, h, b;    // sequence, KV head, block index within the sequence
-  int ns;         // block-sequence index n * NB + b (row block of q / k_blk / out)
-  int sink_tiles, wstart, head;  // context runs of a windowed layer (sched.cuh: CtxSpan)
-  int cost;       // its fixed cost (sched.cuh), cost / 2 places of it before the tiles
-  long long Tu;   // first global place of the unit
-};
-
 __device__ __forceinline__ int clamp_len(const Problem& p, int n, bool report) {
   int L = __ldg(p.ctx_lens + n);
   if (L < 0 || L > p.ctx_stride) {
@@ -59,15 +48,6 @@ __device__ __forceinline__ Unit make_unit(const Problem& p, int u, long long Tu,
 __device__ __forceinline__ Unit next_unit(const Problem& p, const Unit& x) {
   return make_unit(p, x.u + 1, x.Tu + x.tiles + x.cost, x.cost);
 }
-// Global places of the unit's first tile, and behind its last.
-__device__ __forceinline__ long long first_tile(const Unit& x) { return x.Tu + x.cost / 2; }
-__device__ __forceinline__ long long end_tile(const Unit& x) { return first_tile(x) + x.tiles; }
-// Whether no later unit has a tile before `end`, and no earlier one a tile at or after `start`.
-__device__ __forceinline__ bool last_before(const Unit& x, long long end) { return end_tile(x) + x.cost >= end; }
-__device__ __forceinline__ bool first_after(const Unit& x, long long start) {
-  return first_tile(x) - x.cost <= start;
-}
-
 // The boundary table of the call's split, or null for the uniform one.
 __device__ __forceinline__ const long long* range_table(const Problem& p) {
   return p.mode == kDecode ? nullptr : p.causal_starts;
@@ -90,11 +70,10 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
       most = max(most, __reduce_max_sync(0xffffffffu, t));
     }
     T = (long long)p.Hkv * tot;
-    // units of one length over ranges that divide them evenly need no weighing
     const int U = p.B * p.Hkv;
-    if (p.unit_cost > 0 && !(least == most && p.C % U == 0)) cost = fixed_cost(T, U, p.C, p.unit_cost);
+    cost = decode_cost(T, U, p.C, p.unit_cost, least, most);
     T += (long long)U * cost;
-    if (U <= p.C && most <= p.whole_tiles) {
+    if (whole_units(U, p.C, most, p.whole_tiles)) {
       // short units: range c is unit c
       start = end = T;
       if (c >= U) return;
@@ -168,43 +147,6 @@ __device__ __forceinline__ void find_range(const Problem& p, int c, long long& T
     }
     first = make_unit(p, nh * p.NB + lo, (long long)nh * Tnh + p.causal_pref[lo]);
   }
-}
-
-// Segment of the current unit inside [start, end).
-struct Segment {
-  int lo, hi;     // unit-local tiles [lo, hi)
-  bool full;      // covers the whole unit: write the final output
-  int slot;       // partial slot when !full
-  bool last;      // last segment of the range
-};
-
-__device__ __forceinline__ Segment segment_of(const Unit& x, long long start, long long end, int c) {
-  Segment s;
-  const long long f = first_tile(x);
-  s.lo = start > f ? (int)(start - f) : 0;
-  s.hi = end - f < x.tiles ? (int)(end - f) : x.tiles;
-  s.full = (s.lo == 0 && s.hi == x.tiles);
-  s.slot = 2 * c + (s.lo > 0 || first_after(x, start) ? 0 : 1);
-  s.last = last_before(x, end);
-  return s;
-}
-
-// The record of range c: the cut unit that begins in c and runs past its end.
-// C is the plan's range count; the split uses min(C, T) of them.
-__device__ __forceinline__ SplitRecord record_of(const Unit& last, long long T, int C, long long start,
-                                                 long long end, const long long* tab) {
-  C = used_ranges(T, C);
-  SplitRecord r;
-  r.unit = -1;
-  r.last_range = -1;
-  r.first_which = 0;
-  r.pad = 0;
-  if (first_tile(last) >= start && end_tile(last) > end) {
-    r.unit = last.u;
-    r.last_range = range_of_tile_tab(tab, T, C, end_tile(last) - 1);
-    r.first_which = first_after(last, start) ? 0 : 1;
-  }
-  return r;
 }
 
 // Element offset of packed row r of unit x in the final output [.., S, Hq, D].

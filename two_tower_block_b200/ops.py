@@ -37,6 +37,7 @@ EXPORTED_SYMBOLS = [
     "tt_block_attn_block_causal_backward", "tt_confidence_unmask", "tt_block_attn_paged",
     "tt_debug_causal_split", "tt_block_attn_plan_window", "tt_block_attn_tree", "tt_block_attn_tree_paged",
     "tt_kv_append_mx", "tt_kv_read_mx", "tt_block_attn_mx", "tt_debug_mx_scale_words",
+    "tt_debug_decode_split", "tt_debug_causal_split_window",
 ]
 
 
@@ -95,6 +96,8 @@ def lib() -> ctypes.CDLL:
     L.tt_block_attn_mx.argtypes = [vp, vp, cp, vp, vp, vp, vp, vp, vp, vp]
     L.tt_debug_causal_split.argtypes = [i, i, i, i, i, i, i, ctypes.POINTER(ctypes.c_longlong)]
     L.tt_debug_mx_scale_words.argtypes = [i, i, ip, i, ctypes.POINTER(ctypes.c_longlong), ip, ip]
+    L.tt_debug_decode_split.argtypes = [i, ip, i, i, i, i, ctypes.POINTER(ctypes.c_longlong), ip, i, ip, ip, ip]
+    L.tt_debug_causal_split_window.argtypes = [i] * 9 + [ctypes.POINTER(ctypes.c_longlong)]
     L.tt_block_attn_noalloc.argtypes = [ctypes.POINTER(Desc)] + [vp] * 10
     L.tt_selftest_exp2.argtypes = [i, vp, vp, i]
     L.tt_status_string.argtypes = [i]
@@ -695,13 +698,28 @@ def work_split(tiles_per_unit, num_ctas):
     return list(starts), list(first)[:n], list(last)[:n]
 
 
-def causal_split(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost=-1):
+def causal_split(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost=-1, window=0, sinks=0):
     """Host-only: the range boundaries of a block-causal call on the default tcgen05 kernel
     (unit_cost -1: the library's default fixed cost per unit; 0: the even split)."""
     starts = (ctypes.c_longlong * (num_ctas + 1))()
-    _check(lib().tt_debug_causal_split(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost,
-                                       starts), "tt_debug_causal_split")
+    _check(lib().tt_debug_causal_split_window(batch, num_kv_heads, seq_len, block_size, key_tile, num_ctas, unit_cost,
+                                              window, sinks, starts), "tt_debug_causal_split")
     return list(starts)
+
+
+def decode_split(seq_tiles, num_kv_heads, num_ctas, unit_cost=0, whole_tiles=0):
+    """Host-only: the split of a decode call over sequences whose units have seq_tiles[n] tiles, as (range
+    boundaries, cost taken, [(range, unit, first tile, end tile, slot or -1)], [(cut unit or -1, last range,
+    first slot) of each range])."""
+    n = len(seq_tiles)
+    most = n * num_kv_heads + num_ctas
+    starts, rec = (ctypes.c_longlong * (num_ctas + 1))(), (ctypes.c_int * (3 * num_ctas))()
+    seg, cost, num = (ctypes.c_int * (5 * most))(), ctypes.c_int(), ctypes.c_int()
+    _check(lib().tt_debug_decode_split(n, (ctypes.c_int * n)(*seq_tiles), num_kv_heads, num_ctas, unit_cost,
+                                       whole_tiles, starts, rec, most, seg, ctypes.byref(cost), ctypes.byref(num)),
+           "tt_debug_decode_split")
+    return (list(starts), cost.value, [tuple(seg[5 * i:5 * i + 5]) for i in range(num.value)],
+            [tuple(rec[3 * c:3 * c + 3]) for c in range(num_ctas)])
 
 
 def mx_scale_words(head_dim, page_size, slice_rows, count):
