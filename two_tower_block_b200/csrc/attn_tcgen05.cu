@@ -211,13 +211,14 @@ __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* s
   Unit x = sh->first;
   for (; ok;) {
     const Segment sg = segment_of(x, start, end, c);
+    const InnerTiles inner = inner_tiles<NK>(p, x);
     for (int i = max(sg.lo, p.blk_tiles); i < sg.hi; ++i, ++k) {
       const uint32_t slot = k % C::kRaw;
       ok = mbar_wait_warp(smem_u32(&bars->raw_empty[slot]), ((k / C::kRaw) & 1) ^ 1, wc);
       if (!ok) break;
       uint8_t* dst = smem + C::kRawOff + slot * C::kRawBytes;
       const uint32_t bar = smem_u32(&bars->raw_full[slot]);
-      const TileKeys tk = tile_keys(p, x, i);
+      const TileKeys tk = tile_keys<NK>(p, x, inner, i);
       const int mine = min(max(tk.count - (lane << psh), 0), 1 << psh);   // rows of lane's slice
       int row = 0;
       if (mine > 0) {
@@ -288,6 +289,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
   Unit x = sh->first;
   for (; ok;) {
     const Segment sg = segment_of(x, start, end, c);
+    const InnerTiles inner = inner_tiles<NK>(p, x);
     for (int i = sg.lo; i < sg.hi; ++i, ++t) {
       const uint32_t stage = kv * H + t % H;
       const bool blk = i < p.blk_tiles;
@@ -305,7 +307,7 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       ok = mbar_wait_warp(smem_u32(&bars->raw_full[slot]), (k / C::kRaw) & 1, wc);
       if (!ok) break;
       const uint8_t* raw = smem + C::kRawOff + slot * C::kRawBytes;
-      const TileKeys tk = tile_keys(p, x, i);
+      const TileKeys tk = tile_keys<NK>(p, x, inner, i);
       const int n = min(max(round16(tk.count) - first_row, 0), 32);   // rows that the MMAs read
       const int odd = mx_odd(D, p.page_table != nullptr, (x.n * p.Hkv + x.h) * p.ctx_stride + tk.first);
       const uint32_t mask = *reinterpret_cast<const uint32_t*>(raw + C::kRawMask + first_row / 8);
@@ -505,13 +507,14 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         ++q_it;
       }
       const int ctx_row0 = (x.n * p.Hkv + x.h) * p.ctx_stride;
+      const InnerTiles inner = inner_tiles<NK>(p, x);
       // paged cache: a context tile is loaded in slices of psub rows, one per page (pages of
       // at least NK keys hold whole tiles); slices past the tile's last key are not loaded
       const int psub = p.page_table ? min(1 << p.page_shift, NK) : NK;
       // paged context: lane s looks up the pool row of slice s of a tile (one table read per
       // lane, all in flight together), one tile ahead of the loads that use it
       auto slice_row = [&](int i) -> int {
-        const TileKeys tk = tile_keys(p, x, i);
+        const TileKeys tk = tile_keys<NK>(p, x, inner, i);
         if (!p.page_table || tk.is_blk || lane * psub >= tk.count) return 0;
         const int row = paged_row(p, x.n, x.h, tk.first + lane * psub);
         return row < 0 ? (p.num_pages * p.Hkv) << p.page_shift : row;  // a bad page reads as zeros
@@ -519,7 +522,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
       int cur_row = MX ? 0 : slice_row(sg.lo);
       const int hi = MX ? min(sg.hi, p.blk_tiles) : sg.hi;   // (MX: context tiles come from the converters)
       auto load_tile = [&](int i, int kv) {
-        const TileKeys tk = tile_keys(p, x, i);
+        const TileKeys tk = tile_keys<NK>(p, x, inner, i);
         const int box_rows = tk.is_blk ? min(p.S, NK) : (p.page_table ? ceil_div(tk.count, psub) * psub : NK);
         const uint32_t bytes = (uint32_t)(box_rows * kRowBytes * C::kHalves);
         const int nsl = p.page_table && !tk.is_blk ? box_rows / psub : 0;   // slices of a paged tile
@@ -653,6 +656,8 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
     for (; ok;) {
       const Segment sg = segment_of(x, start, end, c);
       const int n = sg.hi - sg.lo;
+      const InnerTiles inner = inner_tiles<NK>(p, x);
+      auto keys16 = [&](int j) { return round16(tile_keys<NK>(p, x, inner, sg.lo + j).count); };
       ok = mbar_wait_warp(smem_u32(&bars->q_full), q_it & 1, wc);
       ++q_it;
       if (!ok) break;
@@ -662,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         ok = kv_wait(tb + j, 0);
         if (!ok) break;
         tc_fence_after();
-        issue_s((G + i) % NBUF, (tb + j) % H, round16(tile_keys(p, x, sg.lo + j).count));
+        issue_s((G + i) % NBUF, (tb + j) % H, keys16(j));
       }
       // (a warp without a tile waits for its accumulator all the same: no phase may be missed)
       if (SPLIT && ok && j0 >= n) ok = mbar_wait_warp(smem_u32(&bars->o_empty[m]), (seg_cnt & 1) ^ 1, wc);
@@ -675,7 +680,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
         if (ok) ok = mbar_wait_warp(smem_u32(&bars->p_full[m][b]), (G / NBUF) & 1, wc);
         if (!ok) break;
         tc_fence_after();
-        const int nv = round16(tile_keys(p, x, sg.lo + j).count);
+        const int nv = keys16(j);
         const uint64_t vd = vdesc0 + (uint64_t)((ev * C::kSlotBytes) >> 4);
         const uint32_t pa = s_tmem + b * NK;
         if (elect_one()) {
@@ -699,7 +704,7 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
           ok = kv_wait(tb + jn, 0);
           if (!ok) break;
           tc_fence_after();
-          issue_s(b, (tb + jn) % H, round16(tile_keys(p, x, sg.lo + jn).count));
+          issue_s(b, (tb + jn) % H, keys16(jn));
         }
       }
       if (!ok) break;
@@ -800,8 +805,9 @@ __global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
           return true;
         };
         const int i0 = sg.lo + (SPLIT ? m : 0);
+        const InnerTiles inner = inner_tiles<NK>(p, x);
         for (int i = i0; i < sg.hi; i += kStep, ++G) {
-          const TileKeys tk = tile_keys(p, x, i);
+          const TileKeys tk = tile_keys<NK>(p, x, inner, i);
           const int count = tk.count;
           unsigned long long mask = 0ull;
           bool full = count == NK;

@@ -210,6 +210,26 @@ __device__ __forceinline__ TileKeys tile_keys(const Problem& p, const Unit& x, i
   return k;
 }
 
+// The unit's inner tiles, whole tiles of visible context keys: those of the window run but its first one where it has a
+// head, and its last one.  Most tiles are, and every role asks about every tile: the short answer there is worth
+// 160.7 -> 157.8 us on the long decode and 4.71 -> 4.49 ms on the block-causal forward.
+struct InnerTiles {
+  int lo;
+  unsigned num;
+  int first;   // position at which unit-local tile 0 would begin if all tiles lay in the window run
+};
+template <int NK>
+__device__ __forceinline__ InnerTiles inner_tiles(const Problem& p, const Unit& x) {
+  const int run = p.blk_tiles + x.sink_tiles, lo = run + (x.head > 0 ? 1 : 0);
+  return {lo, (unsigned)max(x.tiles - 1 - lo, 0), x.wstart - run * NK};
+}
+// tile_keys of a problem whose tiles have NK keys.
+template <int NK>
+__device__ __forceinline__ TileKeys tile_keys(const Problem& p, const Unit& x, const InnerTiles& in, int i) {
+  if ((unsigned)(i - in.lo) < in.num) return {false, in.first + i * NK, NK, 0};
+  return tile_keys(p, x, i);
+}
+
 // Drafted trees: the block rows of tile [first, first + 64) that row t of sequence n sees
 // (itself and its ancestors) as a bit mask; `absent` when the row or one of its ancestors is
 // not there (such a row sees nothing at all).  Parents come before their children, so the walk
