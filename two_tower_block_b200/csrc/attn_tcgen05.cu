@@ -72,7 +72,7 @@ constexpr int kRowBytes = 128;              // one 64-element bf16 row of a swiz
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 constexpr float kNoKey = -1e30f;            // reference maximum of a row that has seen no key yet
 
-template <int D, int NK, bool MX = false, bool SPLIT = false>
+template <int D, int NK, bool VIS = false, bool MX = false, bool SPLIT = false>
 struct Cfg {
   static constexpr int kTreeBytes = kMaxRows * (8 + 2);          // what a tree's rows see, and its walk
   static constexpr int kRows = SPLIT ? 128 : kMaxRows;          // rows of Q in shared memory
@@ -85,12 +85,12 @@ struct Cfg {
   static constexpr int kQBytes = kRows * kRowBytes * kHalves;
   static constexpr int kStageOff = kQBytes;
   static constexpr int kEpiOff = kStageOff + kStages * kSlotBytes;
-  static constexpr int kEpiBytes = 8 * kTreeBytes;   // scratch of the 8 softmax warps
+  static constexpr int kEpiBytes = VIS ? 8 * kTreeBytes : 0;   // trees: scratch of the 8 softmax warps
   static constexpr int kBarOff = kEpiOff + kEpiBytes;
   static constexpr int kBarBytes = 896;
   // MX: the ring of raw tiles: 64 rows of K and of V in e4m3, their scale bytes, a row mask
   static constexpr int kTreeOff = kBarOff + kBarBytes;   // a tree's absent rows, for the V tiles
-  static constexpr int kMlOff = kTreeOff + kMaxRows * 2;   // SPLIT: (maximum, sum) of each row, [2][2][128]
+  static constexpr int kMlOff = kTreeOff + (VIS ? kMaxRows * 2 : 0);   // SPLIT: (maximum, sum) of each row, [2][2][128]
   // MX: word s % kNanSegs is s + 1 if a K row that segment s of the CTA sees holds a NaN.  The converters are
   // at most kStages / 2 + 4 tiles, and so segments, ahead of a softmax warp: the scores of its next two tiles
   // wait for it, and K slots for the scores.
@@ -201,7 +201,7 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
 template <int D, int NK, bool SPLIT>
 __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                                const WaitCtx& wc, int c, int lane) {
-  using C = Cfg<D, NK, true, SPLIT>;
+  using C = Cfg<D, NK, true, true, SPLIT>;
   const uint8_t* src[2] = {reinterpret_cast<const uint8_t*>(p.k_ctx), reinterpret_cast<const uint8_t*>(p.v_ctx)};
   const uint8_t* scales[2] = {p.k_scale, p.v_scale};
   const long long start = sh->start, end = sh->end;
@@ -278,7 +278,7 @@ __device__ __forceinline__ void load_raw_tiles(const Problem& p, const Shared* s
 template <int D, int NK, bool SPLIT>
 __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh, Bars* bars, uint8_t* smem,
                                               const WaitCtx& wc, int c, int w, int lane) {
-  using C = Cfg<D, NK, true, SPLIT>;
+  using C = Cfg<D, NK, true, true, SPLIT>;
   constexpr int H = C::kStages / 2, kRowScale = D / kMxBlock;
   const int kv = w >> 1, first_row = 32 * (w & 1);
   const long long start = sh->start, end = sh->end;
@@ -381,9 +381,9 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
 }
 
 template <int D, int NK, bool VIS, bool MX, bool SPLIT>
-__global__ void __launch_bounds__(Cfg<D, NK, MX, SPLIT>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, NK, VIS, MX, SPLIT>::kThreads, 1)
     attn_tcgen05_kernel(const Problem p, const __grid_constant__ TmaMaps maps) {
-  using C = Cfg<D, NK, MX, SPLIT>;
+  using C = Cfg<D, NK, VIS, MX, SPLIT>;
   constexpr int NBUF = C::kBufs, kThreads = C::kThreads;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -972,7 +972,7 @@ template <int D, int NK, bool VIS, bool MX, bool SPLIT>
 cudaError_t prepare_as() {
   static std::atomic<unsigned long long> done{0};
   return smem_opt_in(reinterpret_cast<const void*>(&attn_tcgen05_kernel<D, NK, VIS, MX, SPLIT>),
-                     Cfg<D, NK, MX, SPLIT>::kSmemBytes, done);
+                     Cfg<D, NK, VIS, MX, SPLIT>::kSmemBytes, done);
 }
 template <int D, bool SPLIT>
 cudaError_t prepare64() {
@@ -989,7 +989,7 @@ cudaError_t prepare(int R) {
 
 template <int D, int NK, bool VIS, bool MX, bool SPLIT>
 cudaError_t launch_as(const Problem& p, const TmaMaps& maps, cudaStream_t stream) {
-  using C = Cfg<D, NK, MX, SPLIT>;
+  using C = Cfg<D, NK, VIS, MX, SPLIT>;
   const cudaError_t e = prepare_as<D, NK, VIS, MX, SPLIT>();
   if (e != cudaSuccess) return e;
   // a programmatic dependent of the previous kernel on the stream (its setup overlaps that
