@@ -128,8 +128,9 @@ TT_API tt_status_t tt_block_attn_plan(const tt_block_attn_desc* desc, int device
  *     { c : 0 <= c < L, c < sinks or c >= L - window }
  * next to the block's own keys (L = ctx_lens[n] for decode, S*b for block b of a block-causal
  * call).  The window slides with the block: all S rows of a block see the same context, and with
- * S = 1 it is the usual per-token window.  Positions outside are not read, except that a paged
- * call may load (and ignore) up to 63 rows in front of the window, within the window's first page.
+ * S = 1 it is the usual per-token window.  What positions outside hold is of no account.  A call may
+ * load some of them all the same, and ignores them: up to 63 rows behind the sinks (inside the
+ * cache), and over pages up to 63 rows in front of the window, within its first page.
  * A call's cost goes with window + sinks, not with L.
  *   window  >= 0; 0: no window (the plan of tt_block_attn_plan; sinks must be 0)
  *   sinks   >= 0; positions that lie in both sets count once

@@ -307,6 +307,11 @@ std::vector<long long> weighted_causal_starts(const std::vector<int>& pref, long
 }
 
 constexpr int kDecodeUnitCost = 5;   // key tiles
+// Up to this many tiles a unit stays whole, where there is a range for each.  Whole it costs its own tiles, one
+// after another; cut it costs the partials' way through L2 and the combine.  For a few units the two meet at 5 to
+// 7 tiles (head_dim 128, whole / cut in a graph: 2 units of 16 rows 9.2 / 9.7 us at 6 tiles, 10.5 / 10.3 at 8;
+// of 256 rows 15.0 / 16.1 at 5, 16.1 / 14.9 at 6).  The more units there are, the less a cut shortens them: 64
+// of 256 rows meet at 11 tiles, 128 beyond 24 (40.4 / 55.2), which this rule leaves.
 constexpr int kWholeUnitTiles = 6;
 
 // Whether a range of its own for every unit is possible (num_ctas set by the caller: not wanted).

@@ -314,13 +314,14 @@ __device__ __forceinline__ void convert_tiles(const Problem& p, const Shared* sh
       const uint8_t* in = raw + (kv * NK + first_row + r4) * D + k4 * 16;
       const uint8_t* sc = raw + C::kRawScale + kv * C::kScaleBytes + (first_row + r4 + odd) * kRowScale + (k4 >> 1);
       uint8_t* to = smem + C::kStageOff + stage * C::kSlotBytes + (first_row + r4) * kRowBytes;
-      // The conversion is bound by the integer pipe (three operations a pair), so the full rows of most
-      // pieces run without selects, and 16 rows at a time with constant offsets from the two halves
-      // of a row in lane's order (one half of head_dim 64).  Not longer: the warps of an SM
-      // sub-partition run different code, and what is unrolled further is waited for as
-      // instruction fetches (a batch of drafted trees: 241 us rolled, 280 with 32 rows at a time).
-      // The look for NaN is two operations a word of four: 16-token blocks over 131072 positions 205 -> 214 us
-      // (looking in the converted pairs or with a second vote: 217 and more).
+      // The full rows of most pieces run without selects, and 16 rows at a time with constant offsets from the
+      // two halves of a row in lane's order (one half of head_dim 64).  What counts is the number of
+      // instructions and the code's length, not a pipe (profiles: the integer pipe is a third busy): the warps of
+      // an SM sub-partition run different code, and what is unrolled further is waited for as instruction
+      // fetches (a batch of drafted trees: 280 us with 32 rows at a time, 257 with 16, 241 rolled, which cost
+      // single tokens a fifth).
+      // The look for NaN is two operations a word of four: 16-token blocks over 131072 positions 205 -> 214 us,
+      // (at the pairs after conversion, or with a vote of its own: 217 and more).
       const int h0 = C::kHalves == 2 ? r4 & 1 : 0;
       auto chunk_in = [&](int h, int r0) { return in + (h0 ^ h) * 64 + r0 * D; };
       auto chunk_sc = [&](int h, int r0) { return sc + (h0 ^ h) * 2 + r0 * kRowScale; };

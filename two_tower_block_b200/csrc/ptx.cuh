@@ -21,10 +21,11 @@ __device__ __forceinline__ unsigned long long globaltimer_ns() {
   asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
   return t;
 }
-// Whether a bounded wait that began at t0 has run past its limit.  Nothing promises that the two halves
-// of the timer are read at once: a read across a carry may be 4.3 s off.  A waiting thread looks
-// every few microseconds, so a time far past the limit is such a read (or the thread was not
-// running): the wait begins anew then, once.
+// Whether a bounded wait that began at t0 has run past its limit.  A wait that seems to be more than a second past
+// it begins anew, once.  The reason is a guess: one call over the quantised cache once reported a timeout that
+// thousands of like ones did not, nothing in the code explained it, and nothing promises that the two halves of
+// the 64-bit timer are read at once (a read across a carry is 4.3 s off).  A wait that is in earnest stuck still
+// ends, at most one limit later.
 __device__ __forceinline__ bool timer_over(unsigned long long& t0, unsigned long long limit_ns, bool& anew) {
   const unsigned long long now = globaltimer_ns();
   if ((long long)(now - t0) <= (long long)limit_ns) return false;
