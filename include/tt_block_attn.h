@@ -345,7 +345,7 @@ TT_API tt_status_t tt_block_attn_noalloc(const tt_block_attn_desc* desc, const v
  *                                  a TT_PLAN_OUT_BF16 plan is rejected (TT_ERR_UNSUPPORTED)
  *   dout [B, N, Hq, D] bf16        dL/dout (a bf16 operand of the tensor cores, like q, k, v)
  *   dq   [B, N, Hq, D] fp32        written
- *   dk_blk, dv_blk [B, N, Hkv, D] fp32   cleared, then written
+ *   dk_blk, dv_blk [B, N, Hkv, D] fp32   written
  * The plan must be a block-causal plan (seq_len > 0).  Asynchronous on `stream`. */
 TT_API tt_status_t tt_block_attn_block_causal_backward(tt_plan_t plan, const void* q, const void* k_ctx,
                                                        const void* v_ctx, const void* k_blk, const void* v_blk,

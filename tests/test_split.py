@@ -106,3 +106,13 @@ def test_windowed_causal_split_refuses_bad_windows():
     for window, sinks in ((-1, 0), (4, -1), (0, 3)):
         with pytest.raises(ops.TTError):
             ops.causal_split(1, 1, 64, 8, 64, 4, -1, window, sinks)
+
+
+def test_a_causal_split_of_the_longest_sequence_is_refused_before_its_table_is_made():
+    """2^31 - 1 blocks: too many tiles, found long before 8 GB of prefix sums are."""
+    import resource
+    before = resource.getrusage(resource.RUSAGE_SELF).ru_maxrss
+    with pytest.raises(ops.TTError) as e:
+        ops.causal_split(1, 1, 2 ** 31 - 1, 1, 64, 4)
+    assert e.value.status == ops.TT_ERR_UNSUPPORTED
+    assert resource.getrusage(resource.RUSAGE_SELF).ru_maxrss - before < 1 << 20   # KB

@@ -479,14 +479,29 @@ std::vector<long long> causal_range_table(const tt_plan_s* P, const std::vector<
 
 // Tiles of one (n, h) before each of its NB blocks, and their sum; false from 2^31 tiles on.
 bool causal_prefix(int NB, int S, int key_tile, int window, int sinks, std::vector<int>& pref) {
-  pref.resize(NB + 1);
+  pref.clear();
   long long acc = 0;
-  for (int b = 0; b <= NB; ++b) {
-    pref[b] = (int)acc;
+  for (int b = 0; b <= NB; ++b) {   // (grown as it goes: a sequence that is too long is found before its end)
+    pref.push_back((int)acc);
     if (b < NB) acc += tt::ceil_div(S, key_tile) + tt::ctx_span(S * b, window, sinks, 1, key_tile).tiles;
     if (acc > (1ll << 31) - 1) return false;
   }
   return true;
+}
+
+// tt_debug_causal_split_window, its arguments checked.
+tt_status_t causal_split(int batch, int num_kv_heads, int NB, int block_size, int key_tile, int num_ctas,
+                         int unit_cost, int window, int sinks, long long* range_start) {
+  std::vector<int> pref;
+  if (!causal_prefix(NB, block_size, key_tile, window, sinks, pref))
+    return fail(TT_ERR_UNSUPPORTED, "sequence too long");
+  const long long T = (long long)batch * num_kv_heads * pref[NB];
+  const std::vector<long long> tab =
+      weighted_causal_starts(pref, (long long)batch * num_kv_heads, num_ctas, unit_cost < 0 ? kCausalUnitCost : unit_cost);
+  const int Ce = tt::used_ranges(T, num_ctas);
+  for (int c = 0; c <= num_ctas; ++c)
+    range_start[c] = c > Ce ? T : tab.empty() ? tt::range_start(T, Ce, c) : tab[c];
+  return TT_OK;
 }
 
 tt_status_t make_plan(const tt_block_attn_desc* desc, int window, int sinks, int device, tt_plan_t* out_plan) {
@@ -1134,17 +1149,12 @@ tt_status_t tt_debug_causal_split_window(int batch, int num_kv_heads, int seq_le
   if (batch < 1 || num_kv_heads < 1 || block_size < 1 || seq_len < block_size || seq_len % block_size != 0 ||
       key_tile < 1 || num_ctas < 1 || window < 0 || sinks < 0 || (sinks > 0 && window == 0) || !range_start)
     return fail(TT_ERR_INVALID_ARG, "bad arguments");
-  const int NB = seq_len / block_size;
-  std::vector<int> pref;
-  if (!causal_prefix(NB, block_size, key_tile, window, sinks, pref))
-    return fail(TT_ERR_UNSUPPORTED, "sequence too long");
-  const long long T = (long long)batch * num_kv_heads * pref[NB];
-  const std::vector<long long> tab =
-      weighted_causal_starts(pref, (long long)batch * num_kv_heads, num_ctas, unit_cost < 0 ? kCausalUnitCost : unit_cost);
-  const int Ce = tt::used_ranges(T, num_ctas);
-  for (int c = 0; c <= num_ctas; ++c)
-    range_start[c] = c > Ce ? T : tab.empty() ? tt::range_start(T, Ce, c) : tab[c];
-  return TT_OK;
+  try {
+    return causal_split(batch, num_kv_heads, seq_len / block_size, block_size, key_tile, num_ctas, unit_cost, window,
+                        sinks, range_start);
+  } catch (const std::exception& e) {
+    return fail(TT_ERR_CUDA, std::string("host allocation: ") + e.what());
+  }
 }
 
 tt_status_t tt_debug_decode_split(int batch, const int* seq_tiles, int num_kv_heads, int num_ctas, int unit_cost,
