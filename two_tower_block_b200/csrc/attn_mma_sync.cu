@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
       if (r >= p.R) continue;
       const float l = half ? l1 : l0;
       const float inv = l > 0.f ? 1.f / l : 0.f;   // a row that saw no key: 0 and lse = -inf
-      const float lse = ((half ? m1 : m0) + __log2f(l)) * 0.6931471805599453f;
+      const float lse2 = (half ? m1 : m0) + __log2f(l);   // log2 units
       const int t = r / p.g, j = r - (r / p.g) * p.g;
       const size_t off = out_offset(p, x, r, D);
 #pragma unroll
@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kThreads) attn_mma_sync_kernel(const Problem p
       if (qq == 0) {
         if (sg.full) {
           if (p.lse)
-            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse;
+            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse2 * kLn2;
         } else {
-          p.part_lse[(size_t)sg.slot * p.R + r] = lse;
+          p.part_lse[(size_t)sg.slot * p.R + r] = lse2;
         }
       }
     }

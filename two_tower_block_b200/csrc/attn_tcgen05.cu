@@ -189,8 +189,18 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const int n = c1 - c0 + 1, i = c - c0;
     const SplitRecord rec{x.u, c1, first_after(x, range_start_tab(tab, T, Ce, c0)) ? 0 : 1, 0};
     const int items = combine_items<D>(p), share = ceil_div(items, n);
+    const int lo = i * share, hi = min(items, lo + share);
+    // as many threads an item as there are, where its segments are many
+    auto parts = [&](auto num) {
+      constexpr int kParts = decltype(num)::value;
+      constexpr int kItems = THREADS / kParts, kWarpItems = 32 / kParts;   // items at a time, of a warp
 #pragma unroll 1
-    for (int it = i * share + tid; it < min(items, (i + 1) * share); it += THREADS) combine_item<D, kGroup>(p, x, c0, rec, it);
+      for (int it = lo + tid / kParts; it < lo + (hi - lo + kWarpItems - 1) / kWarpItems * kWarpItems; it += kItems)
+        combine_item<D, kGroup, kParts>(p, x, c0, rec, min(it, items - 1), it < hi, tid & (kParts - 1));
+    };
+    if (n >= kManySegments && 4 * share <= THREADS) parts(std::integral_constant<int, 4>{});
+    else if (n >= kManySegments && 2 * share <= THREADS) parts(std::integral_constant<int, 2>{});
+    else parts(std::integral_constant<int, 1>{});
   }
 }
 
@@ -930,14 +940,14 @@ __global__ void __launch_bounds__(Cfg<D, NK, VIS, MX, SPLIT>::kThreads, 1)
           }
         }
         if (r < p.R && (!SPLIT || m == 0)) {
-          const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * 0.6931471805599453f;
+          const float lse2 = none ? -INFINITY : m_ref + __log2f(l);   // log2 units
           if (sg.full) {
             if (p.lse) {
               const int t = row_token(r, gm), j = r - t * p.g;
-              p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse;
+              p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse2 * kLn2;
             }
           } else {
-            p.part_lse[(size_t)sg.slot * p.R + r] = lse;
+            p.part_lse[(size_t)sg.slot * p.R + r] = lse2;
           }
         }
         ++seg_cnt;

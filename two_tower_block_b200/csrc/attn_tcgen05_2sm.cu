@@ -551,14 +551,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (w == 0 && r < p.R) {
-        const float lse = (m + __log2f(L)) * 0.6931471805599453f;
+        const float lse2 = m + __log2f(L);   // log2 units
         if (sg.full) {
           if (p.lse) {
             const int t = r / p.g, jj = r - (r / p.g) * p.g;
-            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + jj) * (p.NB * p.S) + x.b * p.S + t] = lse;
+            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + jj) * (p.NB * p.S) + x.b * p.S + t] = lse2 * kLn2;
           }
         } else {
-          p.part_lse[(size_t)sg.slot * p.R + r] = lse;
+          p.part_lse[(size_t)sg.slot * p.R + r] = lse2;
         }
       }
       G += n;

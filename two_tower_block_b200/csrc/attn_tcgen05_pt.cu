@@ -418,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       inv_l[r] = 1.f / l;
       if (r < p.R) {
-        const float lse = (m_ref + __log2f(l)) * 0.6931471805599453f;
+        const float lse2 = m_ref + __log2f(l);   // log2 units
         if (sg.full) {
           if (p.lse) {
             const int t = r / p.g, j = r - (r / p.g) * p.g;
-            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse;
+            p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = lse2 * kLn2;
           }
         } else {
-          p.part_lse[(size_t)sg.slot * p.R + r] = lse;
+          p.part_lse[(size_t)sg.slot * p.R + r] = lse2;
         }
       }
       mbar_arrive(smem_u32(&bars->epi_a));

@@ -22,7 +22,31 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
   if (rec.unit < 0) return;
   const int item = blockIdx.y * kThreads + threadIdx.x;
   if (item >= combine_items<D>(p)) return;
-  combine_item<D>(p, make_unit(p, rec.unit, 0), c, rec, item);
+  combine_item<D, 8, 1>(p, make_unit(p, rec.unit, 0), c, rec, item, true, 0);
+}
+
+// Few units of many segments: block (u, y) does the y-th part of unit u, four threads an item.  It looks for
+// the unit's record among those of all ranges itself, so that no blocks are launched for ranges without one.
+template <int D>
+__global__ void __launch_bounds__(kThreads) combine_few_kernel(const Problem p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ int s_range;
+  __shared__ SplitRecord s_rec;
+  if (threadIdx.x == 0) s_range = -1;
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.C; c += kThreads) {
+    const SplitRecord rec = p.records[c];
+    if (rec.unit == (int)blockIdx.x) {
+      s_rec = rec;
+      s_range = c;
+    }
+  }
+  __syncthreads();
+  const int c = s_range;
+  if (c < 0) return;
+  const int item = blockIdx.y * (kThreads / 4) + threadIdx.x / 4, items = combine_items<D>(p);
+  combine_item<D, 8, 4>(p, make_unit(p, blockIdx.x, 0), c, s_rec, min(item, items - 1), item < items, threadIdx.x & 3);
 }
 
 // One thread waits on a barrier that nothing arrives at; the bounded wait must
@@ -66,7 +90,10 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   // a programmatic dependent launch: the launch overlaps the attention kernel's tail and the
   // kernel waits for the attention grid on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.C, (p.R * (p.D / 8) + kThreads - 1) / kThreads, 1);
+  const long long units = (long long)p.B * p.Hkv * p.NB;
+  const bool few = p.C >= kManySegments * units;
+  const int threads = p.R * (p.D / 8) * (few ? 4 : 1);
+  cfg.gridDim = dim3(few ? (unsigned)units : p.C, (threads + kThreads - 1) / kThreads, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -74,8 +101,8 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (p.D == 128) return cudaLaunchKernelEx(&cfg, combine_kernel<128>, p);
-  return cudaLaunchKernelEx(&cfg, combine_kernel<64>, p);
+  if (p.D == 128) return cudaLaunchKernelEx(&cfg, few ? combine_few_kernel<128> : combine_kernel<128>, p);
+  return cudaLaunchKernelEx(&cfg, few ? combine_few_kernel<64> : combine_kernel<64>, p);
 }
 
 cudaError_t launch_wait_selftest(unsigned* err_word, unsigned long long limit_ns, cudaStream_t stream) {

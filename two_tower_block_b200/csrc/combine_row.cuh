@@ -2,15 +2,19 @@
 // default attention kernel.
 //
 // A cut unit's segments each hold O_s = (sum over its keys of e^{s-m_s} v) / l_s and
-// lse_s = m_s + ln l_s.  The joint softmax over all keys of the unit is recovered
-// exactly: with M = max_s lse_s and w_s = e^{lse_s - M},
-//     out = sum_s w_s O_s / sum_s w_s,     lse = M + ln sum_s w_s.
+// lse_s = (m_s + ln l_s) / ln 2.  The joint softmax over all keys of the unit is recovered
+// exactly: with M = max_s lse_s and w_s = 2^{lse_s - M},
+//     out = sum_s w_s O_s / sum_s w_s,     lse = (M + log2 sum_s w_s) ln 2.
+// (log2 units: the hardware's exponential then takes the difference as it is, within 2 ulp, where one of base e
+// would round its product with log2 e first.)
 // One thread does eight columns of one row (an item; consecutive items are consecutive rows, as the
-// partials lie), with no exchange between threads: it requests kGroup segments' lse values and
-// columns before the first use and folds groups online (running maximum, rescaled sums).  A
-// warp per row, with shuffled weights, took 2.3 us for the first row; what bounds this is one
-// round trip to L2 per group, and with many rows the partials' traffic (eight columns rather than four
-// halve the lse reads and write whole sectors).
+// partials lie): it requests kGroup segments' lse values and columns before the first use and folds groups
+// online (running maximum, rescaled sums).  A warp per row, with shuffled weights, took 2.3 us for the first
+// row; what bounds this is one round trip to L2 per group, and with many rows the partials' traffic (eight
+// columns rather than four halve the lse reads and write whole sectors).
+// kParts: neighbouring threads that share an item, each taking a part of the segments, and join what they have at
+// the end.  One where the segments fit a group; four where a few long units are cut into dozens of segments, whose
+// groups would follow one another (one sequence of 32768 positions, 74 segments a unit: see kManySegments).
 #pragma once
 #include "problem.h"
 #include "ptx.cuh"
@@ -25,11 +29,15 @@ __device__ __forceinline__ int combine_items(const Problem& p) {
   return p.R * (D / 8);
 }
 
+constexpr int kManySegments = 16;   // from here on four threads share an item
+
 // kGroup: 8 (16 cost the separate kernel its occupancy: 64 ragged sequences 67 -> 82 us), 4 in the tail of a
-// kernel whose launch leaves it 128 registers.
-template <int D, int kGroup = 8>
-__device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, int c, const SplitRecord& rec, int item) {
-  const int nseg = rec.last_range - c + 1;
+// kernel whose launch leaves it 128 registers.  With kParts > 1 whole warps call this together; a thread whose
+// item is not `there` only takes part in the joining.
+template <int D, int kGroup, int kParts>
+__device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, int c, const SplitRecord& rec, int item,
+                                             bool there, int part) {
+  const int nseg = there ? rec.last_range - c + 1 : 0;
   const int q = item / p.R, r = item - q * p.R;
   // slot of segment s: 2 c + first_which, 2 (c + 1), 2 (c + 2), ...
   auto slot_of = [&](int s) { return s == 0 ? 2 * c + rec.first_which : 2 * (c + s); };
@@ -38,15 +46,15 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   float M = -INFINITY, wsum = 0.f;
 #pragma unroll 1
-  for (int s0 = 0; s0 < nseg; s0 += kGroup) {
+  for (int s0 = part; s0 < nseg; s0 += kParts * kGroup) {
     float l[kGroup];
     float4 a[kGroup][2];
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
       l[u] = -INFINITY;
       a[u][0] = a[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + u < nseg) {
-        const int slot = slot_of(s0 + u);
+      if (s0 + kParts * u < nseg) {
+        const int slot = slot_of(s0 + kParts * u);
         l[u] = __ldcg(p.part_lse + (size_t)slot * p.R + r);
         const float* src = p.part_o + part_at(p, slot, r, 8 * q, D);
         a[u][0] = __ldcg(reinterpret_cast<const float4*>(src));
@@ -57,14 +65,14 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) Mn = fmaxf(Mn, l[u]);
     // (a row that saw no key in any segment has Mn = -inf: every weight stays 0)
-    const float old = M > -INFINITY ? expf(M - Mn) : 0.f;
+    const float old = M > -INFINITY ? fast_exp2(M - Mn) : 0.f;
     M = Mn;
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc[k] *= old;
     wsum *= old;
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
-      const float w = l[u] != -INFINITY ? expf(l[u] - Mn) : 0.f;   // (a NaN segment spoils the row)
+      const float w = l[u] != -INFINITY ? fast_exp2(l[u] - Mn) : 0.f;   // (a NaN segment spoils the row)
       wsum += w;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -75,6 +83,20 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
       }
     }
   }
+#pragma unroll
+  for (int o = 1; o < kParts; o <<= 1) {
+    const float Mn = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float f = M > -INFINITY ? fast_exp2(M - Mn) : 1.f;   // (nothing yet, or only NaN, is kept as it is)
+    M = Mn;
+    wsum *= f;
+    wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      acc[k] *= f;
+      acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+    }
+  }
+  if (!there || part != 0) return;
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] *= inv;
@@ -91,7 +113,7 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
   }
   if (q == 0 && p.lse) {
     const int t = r / p.g, j = r - (r / p.g) * p.g;
-    p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = M + logf(wsum);
+    p.lse[(size_t)(x.n * p.Hq + x.h * p.g + j) * (p.NB * p.S) + x.b * p.S + t] = (M + log2f(wsum)) * kLn2;
   }
 }
 

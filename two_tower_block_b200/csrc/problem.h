@@ -58,7 +58,7 @@ struct Problem {
                                    // null for the uniform split
   // plan-owned scratch
   float* part_o;        // [2C][D / 4][R][4] (walker.cuh: part_at)
-  float* part_lse;      // [2C][R]
+  float* part_lse;      // [2C][R], in log2 units
   SplitRecord* records; // [C]
   unsigned* err_word;
   unsigned long long wait_limit_ns;

@@ -154,6 +154,7 @@ __device__ __forceinline__ size_t out_offset(const Problem& p, const Unit& x, in
   const int t = r / p.g, j = r - (r / p.g) * p.g;
   return ((size_t)(x.ns * p.S + t) * p.Hq + x.h * p.g + j) * D;
 }
+constexpr float kLn2 = 0.6931471805599453f;   // the kernels' log-sum-exps are in log2 units, partials' too
 // Element offset of columns [col, col + 4) (col a multiple of 4) of packed row r in partial slot `slot`.
 // Four columns of consecutive rows lie together: a warp whose lanes hold rows writes 512 bytes at a
 // time straight from its registers, and a combining warp reads them so.
