@@ -318,14 +318,6 @@ constexpr int kWholeUnitTiles = 6;
 bool whole_units_fit(const tt_block_attn_desc& d, const tt::Problem& p) {
   return d.num_ctas <= 0 && (long long)p.B * p.Hkv * p.NB <= p.C;
 }
-// Tiles of a unit at most.
-long long most_unit_tiles(const tt::Problem& p) {
-  const long long most = p.blk_tiles + (long long)tt::ceil_div(p.ctx_stride, p.key_tile);
-  if (p.window <= 0) return most;
-  // (two runs: a partial tile of the sinks, and a window run that may begin up to a slice early)
-  return std::min(most + 2, p.blk_tiles + 4 + (long long)p.window / p.key_tile + p.sinks / p.key_tile);
-}
-
 // The context of a decode call: contiguous slabs, or pages; bf16, or e4m3 with scales.
 struct CtxCache {
   const void *k, *v;
@@ -409,7 +401,7 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
   }
   // the kernels add up the tiles of all sequences, and those of 32 sequences over all heads, in 32 bits
   // (walker.cuh: find_range), which sequences that share pages could pass
-  const long long most = most_unit_tiles(p);
+  const long long most = tt::most_unit_tiles(p);
   if (most * d.batch > (1ll << 31) - 1 ||
       (most + kDecodeUnitCost) * d.num_kv_heads * std::min(d.batch, 32) > (1ll << 31) - 1)
     return fail(TT_ERR_UNSUPPORTED, "key tiles of the sequences' capacities beyond 2^31");
@@ -862,7 +854,7 @@ tt_status_t tt_block_attn_block_causal(tt_plan_t plan, const void* q, const void
   p.causal_starts = plan->causal_starts;
   bool combine = true;
   if (plan->kernel == TT_KERNEL_TCGEN05 && p.variant == 0 && whole_units_fit(d, p) &&
-      most_unit_tiles(p) <= kWholeUnitTiles) {
+      tt::most_unit_tiles(p) <= kWholeUnitTiles) {
     p.whole_tiles = kWholeUnitTiles;
     p.arrivals = nullptr;
     combine = false;

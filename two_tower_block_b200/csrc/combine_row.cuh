@@ -29,7 +29,7 @@ __device__ __forceinline__ int combine_items(const Problem& p) {
   return p.R * (D / 8);
 }
 
-constexpr int kManySegments = 16;   // from here on four threads share an item
+constexpr int kManySegments = 16;   // from here on several threads may share an item
 
 // kGroup: 8 (16 cost the separate kernel its occupancy: 64 ragged sequences 67 -> 82 us), 4 in the tail of a
 // kernel whose launch leaves it 128 registers.  With kParts > 1 whole warps call this together; a thread whose

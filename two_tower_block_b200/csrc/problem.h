@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "sched.cuh"
 
 namespace tt {
@@ -78,6 +80,14 @@ struct Problem {
   int pages_per_seq;
   int num_pages;
 };
+
+// Tiles of a unit at most.
+inline long long most_unit_tiles(const Problem& p) {
+  const long long most = p.blk_tiles + (long long)ceil_div(p.ctx_stride, p.key_tile);
+  if (p.window <= 0) return most;
+  // (two runs: a partial tile of the sinks, and a window run that may begin up to a slice early)
+  return std::min(most + 2, p.blk_tiles + 4 + (long long)p.window / p.key_tile + p.sinks / p.key_tile);
+}
 
 // Host launchers (each returns the cudaError_t of its launch).
 cudaError_t launch_attn_mma_sync(const Problem& p, cudaStream_t stream);
