@@ -190,17 +190,12 @@ __device__ __forceinline__ void fused_combine(const Problem& p, long long T, lon
     const SplitRecord rec{x.u, c1, first_after(x, range_start_tab(tab, T, Ce, c0)) ? 0 : 1, 0};
     const int items = combine_items<D>(p), share = ceil_div(items, n);
     const int lo = i * share, hi = min(items, lo + share);
-    // as many threads an item as there are, where its segments are many
-    auto parts = [&](auto num) {
-      constexpr int kParts = decltype(num)::value;
-      constexpr int kItems = THREADS / kParts, kWarpItems = 32 / kParts;   // items at a time, of a warp
+    // as many threads an item as there are, where its segments are many; whole warps stay together
+    const int sh = n < kManySegments ? 0 : 4 * share <= THREADS ? 2 : 2 * share <= THREADS ? 1 : 0;
+    const int warp_items = 32 >> sh;
 #pragma unroll 1
-      for (int it = lo + tid / kParts; it < lo + (hi - lo + kWarpItems - 1) / kWarpItems * kWarpItems; it += kItems)
-        combine_item<D, kGroup, kParts>(p, x, c0, rec, min(it, items - 1), it < hi, tid & (kParts - 1));
-    };
-    if (n >= kManySegments && 4 * share <= THREADS) parts(std::integral_constant<int, 4>{});
-    else if (n >= kManySegments && 2 * share <= THREADS) parts(std::integral_constant<int, 2>{});
-    else parts(std::integral_constant<int, 1>{});
+    for (int it = lo + (tid >> sh); it < lo + (hi - lo + warp_items - 1) / warp_items * warp_items; it += THREADS >> sh)
+      combine_item<D, kGroup>(p, x, c0, rec, min(it, items - 1), it < hi, 1 << sh, tid & ((1 << sh) - 1));
   }
 }
 

@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
   if (rec.unit < 0) return;
   const int item = blockIdx.y * kThreads + threadIdx.x;
   if (item >= combine_items<D>(p)) return;
-  combine_item<D, 8, 1>(p, make_unit(p, rec.unit, 0), c, rec, item, true, 0);
+  combine_item<D, 8>(p, make_unit(p, rec.unit, 0), c, rec, item, true, 1, 0);
 }
 
 // Few units of many segments: block (u, y) does the y-th part of unit u, four threads an item.  It looks for
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kThreads) combine_few_kernel(const Problem p) 
   const int c = s_range;
   if (c < 0) return;
   const int item = blockIdx.y * (kThreads / 4) + threadIdx.x / 4, items = combine_items<D>(p);
-  combine_item<D, 8, 4>(p, make_unit(p, blockIdx.x, 0), c, s_rec, min(item, items - 1), item < items, threadIdx.x & 3);
+  combine_item<D, 8>(p, make_unit(p, blockIdx.x, 0), c, s_rec, min(item, items - 1), item < items, 4, threadIdx.x & 3);
 }
 
 // One thread waits on a barrier that nothing arrives at; the bounded wait must

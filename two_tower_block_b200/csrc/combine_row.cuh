@@ -12,7 +12,7 @@
 // online (running maximum, rescaled sums).  A warp per row, with shuffled weights, took 2.3 us for the first
 // row; what bounds this is one round trip to L2 per group, and with many rows the partials' traffic (eight
 // columns rather than four halve the lse reads and write whole sectors).
-// kParts: neighbouring threads that share an item, each taking a part of the segments, and join what they have at
+// `parts`: neighbouring threads (1, 2 or 4) that share an item, each taking a part of the segments, and join what they have at
 // the end.  One where the segments fit a group; four where a few long units are cut into dozens of segments, whose
 // groups would follow one another (one sequence of 32768 positions, 74 segments a unit: see kManySegments).
 #pragma once
@@ -32,11 +32,11 @@ __device__ __forceinline__ int combine_items(const Problem& p) {
 constexpr int kManySegments = 16;   // from here on several threads may share an item
 
 // kGroup: 8 (16 cost the separate kernel its occupancy: 64 ragged sequences 67 -> 82 us), 4 in the tail of a
-// kernel whose launch leaves it 128 registers.  With kParts > 1 whole warps call this together; a thread whose
+// kernel whose launch leaves it 128 registers.  With parts > 1 whole warps call this together; a thread whose
 // item is not `there` only takes part in the joining.
-template <int D, int kGroup, int kParts>
+template <int D, int kGroup>
 __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, int c, const SplitRecord& rec, int item,
-                                             bool there, int part) {
+                                             bool there, int parts, int part) {
   const int nseg = there ? rec.last_range - c + 1 : 0;
   const int q = item / p.R, r = item - q * p.R;
   // slot of segment s: 2 c + first_which, 2 (c + 1), 2 (c + 2), ...
@@ -46,15 +46,15 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   float M = -INFINITY, wsum = 0.f;
 #pragma unroll 1
-  for (int s0 = part; s0 < nseg; s0 += kParts * kGroup) {
+  for (int s0 = part; s0 < nseg; s0 += parts * kGroup) {
     float l[kGroup];
     float4 a[kGroup][2];
 #pragma unroll
     for (int u = 0; u < kGroup; ++u) {
       l[u] = -INFINITY;
       a[u][0] = a[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (s0 + kParts * u < nseg) {
-        const int slot = slot_of(s0 + kParts * u);
+      if (s0 + parts * u < nseg) {
+        const int slot = slot_of(s0 + parts * u);
         l[u] = __ldcg(p.part_lse + (size_t)slot * p.R + r);
         const float* src = p.part_o + part_at(p, slot, r, 8 * q, D);
         a[u][0] = __ldcg(reinterpret_cast<const float4*>(src));
@@ -83,8 +83,8 @@ __device__ __forceinline__ void combine_item(const Problem& p, const Unit& x, in
       }
     }
   }
-#pragma unroll
-  for (int o = 1; o < kParts; o <<= 1) {
+#pragma unroll 1
+  for (int o = 1; o < parts; o <<= 1) {
     const float Mn = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     const float f = M > -INFINITY ? fast_exp2(M - Mn) : 1.f;   // (nothing yet, or only NaN, is kept as it is)
     M = Mn;
