@@ -47,3 +47,23 @@ def test_few_long_units(S, g, D, lens, tree, kernel):
     assert not out.cpu().numpy()[gone.transpose(0, 2, 1)].any()
     assert_parity(out, ro, "out")
     assert_parity(torch.where(torch.isinf(lse), torch.zeros_like(lse), lse), np.where(gone, 0.0, rl), "lse")
+
+
+@pytest.mark.parametrize("kernel", KERNELS[:3] + KERNELS[-1:])
+@pytest.mark.parametrize("B,Hkv", [(4, 1), (40, 2), (64, 2)])
+def test_short_lengths_in_a_large_capacity(B, Hkv, kernel):
+    """Units of at most six tiles, which the capacity does not tell: cut where they are few, whole where they are
+    many; then the same plan with one long sequence among them."""
+    S, g, D, cap = 4, 4, 64, 2000
+    rng = np.random.default_rng(103)
+    plan = make_plan(kernel, B, g * Hkv, Hkv, D, S, ctx_capacity=cap)
+    for longest in (300, 2000, 300):
+        lens = [int(x) for x in rng.integers(0, 300, B)]
+        lens[1] = longest
+        inp = make_decode(B, S, g * Hkv, Hkv, D, cap, seed=104, ctx_lens=lens)
+        x = [dev(t) for t in (inp.q, poison_beyond(inp.k_ctx, lens), poison_beyond(inp.v_ctx, lens), inp.k_blk, inp.v_blk)]
+        out, lse = plan.block_attn(*x, i32(lens), want_lse=True)
+        plan.check()
+        ro, rl = vis.block_attn_visible(f64(inp.q), f64(inp.k_ctx), f64(inp.v_ctx), f64(inp.k_blk), f64(inp.v_blk), lens)
+        assert_parity(out, ro, f"out, longest {longest}")
+        assert_parity(lse, rl, f"lse, longest {longest}")

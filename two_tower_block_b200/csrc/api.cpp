@@ -416,10 +416,16 @@ tt_status_t decode_call(tt_plan_t plan, const void* q, const CtxCache& c, const 
     // ragged batches: a unit costs about five tiles beyond its own (sched.cuh) on the default kernel
     p.unit_cost = kDecodeUnitCost;
     // short contexts: a cut costs a partial and its combine, whole units only their own tiles
-    if (whole_units_fit(d, p)) p.whole_tiles = kWholeUnitTiles;
-    if (most <= p.whole_tiles) {   // no length can cut one: nothing to combine
-      p.arrivals = nullptr;
-      combine = false;
+    if (whole_units_fit(d, p)) {
+      if (most <= kWholeUnitTiles) {   // no length can cut one: nothing to combine
+        p.whole_tiles = kWholeUnitTiles;
+        p.arrivals = nullptr;
+        combine = false;
+      } else if (2ll * p.B * p.Hkv >= p.C) {
+        // the lengths decide, on the device, and the combine is launched whatever they say: whole pays where cuts
+        // would not shorten the units much (4 units of 8 rows and 6 tiles: cut 10.6 us, whole 12.5)
+        p.whole_tiles = kWholeUnitTiles;
+      }
     }
   }
   p.ctx_lens = ctx_lens;
