@@ -9,6 +9,7 @@ namespace tt {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kFewUnitsSegments = 48;   // segments of a unit from which on combine_few_kernel runs
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) combine_kernel(const Problem p) {
@@ -91,8 +92,9 @@ cudaError_t launch_combine(const Problem& p, cudaStream_t stream) {
   // kernel waits for the attention grid on the device
   cudaLaunchConfig_t cfg = {};
   const long long units = (long long)p.B * p.Hkv * p.NB;
-  // (looking for the record costs 0.6 us: units of 15 tiles 11.7 -> 12.3 us, of 26 13.2 -> 12.8, of 129 19.3 -> 17.5)
-  const bool few = p.C >= kManySegments * units && most_unit_tiles(p) >= 20;
+  // (looking for the record costs 0.6 us, which few segments do not win back: 2 units of 35 tiles 13.7 -> 14.4 us, of 129
+  // 19.3 -> 17.5)
+  const bool few = p.C >= kFewUnitsSegments * units && most_unit_tiles(p) >= kFewUnitsSegments;
   const int threads = p.R * (p.D / 8) * (few ? 4 : 1);
   cfg.gridDim = dim3(few ? (unsigned)units : p.C, (threads + kThreads - 1) / kThreads, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
