@@ -72,7 +72,7 @@ def _build_marshal(binding):
     try:
         r = subprocess.run(_marshal_cmd(binding), capture_output=True, text=True)
         why = r.stderr if r.returncode != 0 else None
-    except (OSError, ImportError) as e:
+    except (OSError, ImportError, AttributeError) as e:   # (AttributeError: a torch that is not whole)
         why = str(e)
     if why is None:
         os.replace(MARSHAL + ".tmp", MARSHAL)
