@@ -35,7 +35,7 @@
  *     are fp32; ctx_lens is int32.  Every tensor pointer must be 16-byte
  *     aligned (the unmasking step's int / float arrays: 4-byte).
  *   - What a row sees has to be finite: with a NaN or an infinity among the bf16 values that its softmax
- *     takes in, the row's results are unspecified.  Positions that it does not see may hold anything.
+ *     takes in, the row's results are unspecified.  Positions that no row of a block sees may hold anything.
  *   - Calls are asynchronous and ordered on `stream`; none synchronises the
  *     host except tt_block_attn_check and tt_block_attn_profile_read.
  *   - A plan may be used by one stream at a time (it owns scratch memory).
@@ -209,8 +209,9 @@ TT_API tt_status_t tt_block_attn_paged(tt_plan_t plan, const void* q, const void
  *   parents [B, S] int32 (device): parents[n][t] is the row that row t hangs on, 0 <= parent < t;
  *           -1: it hangs on the last committed token; -2: row t is absent (a sequence that
  *           drafted fewer than S tokens).  A row whose ancestor is absent is absent too.
- * An absent row's output is 0 and its lse -inf, and its q, k_blk and v_blk may hold anything.  An
- * entry >= t or < -2 is flagged TT_ERR_DEVICE_ARG and its row taken as absent.
+ * An absent row's output is 0 and its lse -inf, and its q, k_blk and v_blk may hold anything.  The v_blk of
+ * rows that are there has to be finite for the sake of other branches too (a weight of 0 does not hide an
+ * infinity).  An entry >= t or < -2 is flagged TT_ERR_DEVICE_ARG and its row taken as absent.
  * Everything else as tt_block_attn; runs the default tcgen05 kernel (64-key tiles) or the
  * mma.sync kernel, as the plan chose. */
 TT_API tt_status_t tt_block_attn_tree(tt_plan_t plan, const void* q, const void* k_ctx, const void* v_ctx,
